@@ -33,6 +33,7 @@
 #include <new>
 
 #include "../../include/qgemv.h"
+#include "../../include/qgemv_epilogue.h"
 #include "qgemv_decode.h"
 #include "qgemv_internal.h"
 #include "qgemv_layout.h"
@@ -329,14 +330,105 @@ __device__ __forceinline__ void lds_barrier() {
 // registers, then clears what it wrote.
 // ---------------------------------------------------------------------------
 constexpr int kWaves = 16;
+
+// ---------------------------------------------------------------------------
+// Epilogue of a product: t = (W x)[row] + bias[row], then act(t) or, gated,
+// act(t[2i]) * t[2i + 1] with the gate and up rows interleaved, plus the
+// residual, rounded once to the output type.  It runs on the fp32 sums that
+// the kernel holds anyway, so it moves only its own operands: the bias and
+// residual are read and y written once, by the thread that owns the output
+// (a residual that is y itself is read before it is written).  Every kernel
+// is built with and without it, so that a plain product's code stays as it is.
+// ---------------------------------------------------------------------------
+template <bool EPI>
+struct EpiArg {};
+
+template <>
+struct EpiArg<true> {
+  const void* bias;
+  const void* residual;
+  void* y;
+  int64_t ldy, ldr;  // elements between batch rows
+  int act, gated, y32, bias32, res32;
+
+  static __device__ __forceinline__ float load(const void* p, int f32, int64_t i) {
+    return f32 ? ((const float*)p)[i] : (float)((const _Float16*)p)[i];
+  }
+  __device__ __forceinline__ float biased(float v, int row) const { return bias ? v + load(bias, bias32, row) : v; }
+  __device__ __forceinline__ float activate(float t) const {
+    switch (act) {
+      case QGEMV_ACT_RELU: return t < 0.f ? 0.f : t;  // a NaN stays one
+      case QGEMV_ACT_GELU: return 0.5f * t * (1.f + erff(t * 0.70710678f));
+      case QGEMV_ACT_GELU_TANH: return 0.5f * t * (1.f + tanhf(0.79788456f * (t + 0.044715f * t * t * t)));
+      case QGEMV_ACT_SILU: return t / (1.f + expf(-t));
+      default: return t;
+    }
+  }
+  __device__ __forceinline__ void store(int n, int col, float v) const {
+    if (residual) v += load(residual, res32, n * ldr + col);
+    if (y32) ((float*)y)[n * ldy + col] = v;
+    else ((_Float16*)y)[n * ldy + col] = (_Float16)v;
+  }
+  __device__ __forceinline__ void put(int n, int row, float v) const { store(n, row, activate(biased(v, row))); }
+  // row is even; g and u are the sums of rows row and row + 1
+  __device__ __forceinline__ void put_gated(int n, int row, float g, float u) const {
+    store(n, row >> 1, activate(biased(g, row)) * biased(u, row + 1));
+  }
+};
+
+// Write the workgroup's nrows x NB outputs; sum(r, n) gives local row r of batch row n.
+template <int NB, bool EPI, class Sum>
+__device__ __forceinline__ void write_rows(const EpiArg<EPI>& ep, float* y, int M, int T0, int nrows, Sum sum) {
+  if constexpr (EPI) {
+    if (ep.gated) {  // M is even, so a workgroup's rows are whole pairs
+      for (int i = threadIdx.x; i < nrows / 2 * NB; i += 64 * kWaves) {
+        const int r = 2 * (i / NB), n = i % NB;
+        ep.put_gated(n, T0 * 16 + r, sum(r, n), sum(r + 1, n));
+      }
+      return;
+    }
+  }
+  for (int i = threadIdx.x; i < nrows * NB; i += 64 * kWaves) {
+    const int r = i / NB, n = i % NB;
+    const float v = sum(r, n);
+    if constexpr (EPI) ep.put(n, T0 * 16 + r, v);
+    else y[(size_t)n * M + T0 * 16 + r] = v;
+  }
+}
+
+// The same where sum(r, n4) gives batch rows n4 .. n4 + 3 of local row r.
+template <int NB, bool EPI, class Sum>
+__device__ __forceinline__ void write_rows4(const EpiArg<EPI>& ep, float* y, int M, int T0, int nrows, Sum sum) {
+  if constexpr (EPI) {
+    if (ep.gated) {
+      for (int i = threadIdx.x; i < nrows / 2 * NB / 4; i += 64 * kWaves) {
+        const int r = 2 * (i / (NB / 4)), n4 = 4 * (i % (NB / 4));
+        const floatx4_t g = sum(r, n4), u = sum(r + 1, n4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ep.put_gated(n4 + k, T0 * 16 + r, g[k], u[k]);
+      }
+      return;
+    }
+  }
+  for (int i = threadIdx.x; i < nrows * NB / 4; i += 64 * kWaves) {
+    const int r = i / (NB / 4), n4 = 4 * (i - r * (NB / 4));
+    const floatx4_t v = sum(r, n4);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (EPI) ep.put(n4 + k, T0 * 16 + r, v[k]);
+      else y[(size_t)(n4 + k) * M + T0 * 16 + r] = v[k];
+    }
+  }
+}
+
 constexpr uint32_t kVmcntZero = 0x0F70;  // s_waitcnt vmcnt(0), no wait on the other counters
 
-template <int FMT, int BITS, int CH, int NR, int NB, bool XST>
+template <int FMT, int BITS, int CH, int NR, int NB, bool XST, bool EPI>
 __global__ void __launch_bounds__(64 * kWaves)
 k_stream(const uint8_t* __restrict__ codes, const uint32_t* __restrict__ meta, const int32_t* __restrict__ row_ptr,
          const uint32_t* __restrict__ entries, const int32_t* __restrict__ boff, const uint32_t* __restrict__ bent,
          const uint16_t* __restrict__ x, float* __restrict__ y, int M, int K, int Kp, int nkb, int tiles,
-         uint32_t codes_bytes, uint32_t meta_bytes, int nnz, int ent_cap, int gsz) {
+         uint32_t codes_bytes, uint32_t meta_bytes, int nnz, int ent_cap, int gsz, EpiArg<EPI> ep) {
   using F = Fmt<FMT, BITS>;
   constexpr int BB = 256 * BITS;
   constexpr bool B1 = NB == 1;
@@ -808,16 +900,24 @@ k_stream(const uint8_t* __restrict__ codes, const uint32_t* __restrict__ meta, c
       v += dpp_mov<0x4E, 0xF>(v);   // quad_perm [2,3,0,1]
       v += dpp_mov<0x141, 0xF>(v);  // row_half_mirror
       v += dpp_mov<0x140, 0xF>(v);  // row_mirror: every lane of the row holds the sum
-      if (r < nrows && sl == 0) y[T0 * 16 + r] = v;
+      if constexpr (EPI) {
+        // rows r and r ^ 1 sit in neighbouring 16-lane rows of the wave
+        const float u = __shfl_xor(v, 16);
+        if (r < nrows && sl == 0) {
+          if (!ep.gated) ep.put(0, T0 * 16 + r, v);
+          else if (!(r & 1)) ep.put_gated(0, T0 * 16 + r, v, u);
+        }
+      } else {
+        if (r < nrows && sl == 0) y[T0 * 16 + r] = v;
+      }
     }
   } else {
-    for (int i = threadIdx.x; i < nrows * NB; i += 64 * kWaves) {
-      const int r = i / NB, n = i % NB;
+    write_rows<NB, EPI>(ep, y, M, T0, nrows, [&](int r, int n) {
       const float* pr = part + (r >> 4) * CPT * 16 * NB + (r & 15) * NB + n;
       float v = 0.f;
       for (int j = 0; j < CPT; ++j) v += pr[j * 16 * NB];
-      y[(size_t)n * M + T0 * 16 + r] = v;
-    }
+      return v;
+    });
   }
 }
 
@@ -838,11 +938,12 @@ k_stream(const uint8_t* __restrict__ codes, const uint32_t* __restrict__ meta, c
 // slots of the waves covering its tile in wave order, then the outliers, so
 // the result does not depend on timing.
 // ---------------------------------------------------------------------------
-template <int FMT, int BITS, int NB, int R>
+template <int FMT, int BITS, int NB, int R, bool EPI>
 __global__ void __launch_bounds__(64 * kWaves)
 k_xlds(const uint8_t* __restrict__ codes, const uint32_t* __restrict__ meta, const int32_t* __restrict__ row_ptr,
        const uint32_t* __restrict__ entries, const uint16_t* __restrict__ x, float* __restrict__ y, int M, int K,
-       int Kp, int nkb, int tiles, uint32_t codes_bytes, uint32_t meta_bytes, int nnz, int ent_cap, int gsz) {
+       int Kp, int nkb, int tiles, uint32_t codes_bytes, uint32_t meta_bytes, int nnz, int ent_cap, int gsz,
+       EpiArg<EPI> ep) {
   using F = Fmt<FMT, BITS>;
   constexpr int BB = 256 * BITS;
   constexpr int NP = NB / 2;
@@ -1067,8 +1168,8 @@ k_xlds(const uint8_t* __restrict__ codes, const uint32_t* __restrict__ meta, con
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < nrows * NB; i += 64 * kWaves) {
-    const int r = i / NB, n = i % NB, t = r >> 4;
+  write_rows<NB, EPI>(ep, y, M, T0, nrows, [&](int r, int n) {
+    const int t = r >> 4;
     // Every slot is read before the first add (slots past the runs are in
     // bounds and dropped by the select), so the reads overlap instead of
     // waiting one by one inside a branch.
@@ -1078,8 +1179,8 @@ k_xlds(const uint8_t* __restrict__ codes, const uint32_t* __restrict__ meta, con
     float v = 0.f;
 #pragma unroll
     for (int u = 0; u < kWaves; ++u) v = runs[2 * u] <= t && t <= runs[2 * u + 1] ? v + s[u] : v;
-    y[(size_t)n * M + T0 * 16 + r] = v + csr[i];
-  }
+    return v + csr[r * NB + n];
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -1109,12 +1210,12 @@ k_xlds(const uint8_t* __restrict__ codes, const uint32_t* __restrict__ meta, con
 // and the arrival that reaches the next multiple is the last: nothing needs
 // clearing.
 // ---------------------------------------------------------------------------
-template <int FMT, int BITS, int NB, int CH>
+template <int FMT, int BITS, int NB, int CH, bool EPI>
 __global__ void __launch_bounds__(64 * kWaves)
 k_split(const uint8_t* __restrict__ codes, const uint32_t* __restrict__ meta, const int32_t* __restrict__ boff,
         const uint32_t* __restrict__ bent, const uint16_t* __restrict__ x, float* __restrict__ y,
         float* __restrict__ wpart, uint32_t* __restrict__ wctr, int M, int K, int nkb, int tiles,
-        uint32_t codes_bytes, uint32_t meta_bytes, int nnz, int gsz, int S, int NG) {
+        uint32_t codes_bytes, uint32_t meta_bytes, int nnz, int gsz, int S, int NG, EpiArg<EPI> ep) {
   using F = Fmt<FMT, BITS>;
   constexpr int BB = 256 * BITS;
   extern __shared__ uint32_t lds[];
@@ -1361,20 +1462,22 @@ k_split(const uint8_t* __restrict__ codes, const uint32_t* __restrict__ meta, co
   constexpr int kSc1 = 16;  // cache policy: device-coherent (bypass the XCD's non-coherent L2 copy)
   const rsrc_t rw = make_rsrc(wpart, (uint32_t)((uint64_t)S * tiles * 16 * NB * 4));
   const uint32_t wbase = (uint32_t)((si * tiles + T0) * 16 * NB) * 4u;  // this split's partials of the group
-  for (int i = threadIdx.x; i < nrows * NB / 4; i += 64 * kWaves) {
-    const int r = i / (NB / 4), n4 = 4 * (i - r * (NB / 4));
+  auto own_sum = [&](int r, int n4) {
     const float* ps = part + (r >> 4) * CPT * 16 * NB + (r & 15) * NB + n4;
     floatx4_t v = {0.f, 0.f, 0.f, 0.f};
     for (int j = 0; j < CPT; ++j) v += *(const floatx4_t*)(ps + j * 16 * NB);
-    if (split) {
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), rw, (int)(wbase + 16u * (uint32_t)i), 0,
-                                             kSc1);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) y[(size_t)(n4 + k) * M + T0 * 16 + r] = v[k];
-    }
+    return v;
+  };
+  if (!split) {
+    write_rows4<NB, EPI>(ep, y, M, T0, nrows, own_sum);
+    return;
   }
-  if (!split) return;
+  for (int i = threadIdx.x; i < nrows * NB / 4; i += 64 * kWaves) {
+    const int r = i / (NB / 4), n4 = 4 * (i - r * (NB / 4));
+    const floatx4_t v = own_sum(r, n4);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), rw, (int)(wbase + 16u * (uint32_t)i), 0,
+                                           kSc1);
+  }
 
   // The splits meet.  The partials went out as device-coherent stores; each
   // thread waits until its stores are acknowledged, and after the barrier
@@ -1390,21 +1493,20 @@ k_split(const uint8_t* __restrict__ codes, const uint32_t* __restrict__ meta, co
   }
   __syncthreads();
   if (!*last_flag) return;
-  for (int i = threadIdx.x; i < nrows * NB / 4; i += 64 * kWaves) {
-    const int r = i / (NB / 4), n4 = 4 * (i - r * (NB / 4));
+  write_rows4<NB, EPI>(ep, y, M, T0, nrows, [&](int r, int n4) {
+    const uint32_t i = (uint32_t)(r * NB + n4) / 4u;
     u32x4_t pv[8];
 #pragma unroll
     for (int s2 = 0; s2 < 8; ++s2)
       pv[s2] = __builtin_amdgcn_raw_buffer_load_b128(
-          rw, s2 < S ? (int)((uint32_t)((s2 * tiles + T0) * 16 * NB) * 4u + 16u * (uint32_t)i) : (int)kOutOfRange, 0,
+          rw, s2 < S ? (int)((uint32_t)((s2 * tiles + T0) * 16 * NB) * 4u + 16u * i) : (int)kOutOfRange, 0,
           kSc1);
     floatx4_t v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int s2 = 0; s2 < 8; ++s2)
       if (s2 < S) v += __builtin_bit_cast(floatx4_t, pv[s2]);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) y[(size_t)(n4 + k) * M + T0 * 16 + r] = v[k];
-  }
+    return v;
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -1431,11 +1533,11 @@ k_split(const uint8_t* __restrict__ codes, const uint32_t* __restrict__ meta, co
 // of the waves covering its region in wave order, then its outliers, so the
 // result does not depend on timing.
 // ---------------------------------------------------------------------------
-template <int R>
+template <int R, bool EPI>
 __global__ void __launch_bounds__(64 * kWaves)
 k_pair(const uint8_t* __restrict__ codes, const uint32_t* __restrict__ meta, const int32_t* __restrict__ row_ptr,
        const uint32_t* __restrict__ entries, const uint16_t* __restrict__ x, float* __restrict__ y, int M, int K,
-       int Kp, int nkb, int tiles, uint32_t meta_bytes) {
+       int Kp, int nkb, int tiles, uint32_t meta_bytes, EpiArg<EPI> ep) {
   extern __shared__ uint32_t lds[];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1611,7 +1713,7 @@ k_pair(const uint8_t* __restrict__ codes, const uint32_t* __restrict__ meta, con
     }
   }
   __syncthreads();
-  for (int r = threadIdx.x; r < nrows; r += 64 * kWaves) {
+  write_rows<1, EPI>(ep, y, M, T0, nrows, [&](int r, int) {
     const int g = r >> 6;  // local row r = 64 g + 16 t + m
     float s[kWaves];  // all reads first, then the adds in wave order
 #pragma unroll
@@ -1622,8 +1724,8 @@ k_pair(const uint8_t* __restrict__ codes, const uint32_t* __restrict__ meta, con
       const int c0 = run_bound(u), c1 = run_bound(u + 1);
       v = c0 < c1 && c0 < (g + 1) * P && c1 > g * P ? v + s[u] : v;
     }
-    y[T0 * 16 + r] = v + csr[r];
-  }
+    return v + csr[r];
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -1659,12 +1761,12 @@ static_assert(kWaves == 16 && kHuffTable * 16 == 4 * 1024 && kMaxK / 8 <= 2 * 10
                   kHuffMaxSub * kHuffSub / 4 <= 4 * 1024,
               "the prologue stages x, the tables and the second-level tables in fixed rounds of 1024 threads");
 
-template <int G, bool SUB, int NB>
+template <int G, bool SUB, int NB, bool EPI>
 __global__ void __launch_bounds__(64 * kWaves)
 k_huff(const uint32_t* __restrict__ words, const uint16_t* __restrict__ steps, const uint32_t* __restrict__ hidx,
        const uint16_t* __restrict__ hlane, const int32_t* __restrict__ htab, const int16_t* __restrict__ hsym,
        const uint16_t* __restrict__ x, float* __restrict__ y, int M, int K, int nkb, int tiles, int nsym,
-       uint32_t nwords, int bufw, int nsub) {
+       uint32_t nwords, int bufw, int nsub, EpiArg<EPI> ep) {
   extern __shared__ uint32_t lds[];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1904,15 +2006,15 @@ k_huff(const uint32_t* __restrict__ words, const uint16_t* __restrict__ steps, c
   }
   if (b0 < b1) flush();
   __syncthreads();
-  for (int i = threadIdx.x; i < nrows * NB; i += 64 * kWaves) {
-    const int r = NB == 1 ? i : i / NB, n = NB == 1 ? 0 : i - r * NB, t = r >> 4;
+  write_rows<NB, EPI>(ep, y, M, T0, nrows, [&](int r, int n) {
+    const int t = r >> 4;
     float v = 0.f;
     for (int u = 0; u < kWaves; ++u) {
       const int c0 = u * L / kWaves, c1 = (u + 1) * L / kWaves;
       if (c0 < c1 && c0 / nkb <= t && t <= (c1 - 1) / nkb) v += slots[((u + t) * 16 + (r & 15)) * NB + n];
     }
-    y[n * M + T0 * 16 + r] = v;
-  }
+    return v;
+  });
 }
 
 // Debug: decode the blob's codes back to canonical order, one thread per 32-code chunk.
@@ -2040,8 +2142,8 @@ bool stream_xst(const BlobHeader& h, int nb, int ch) {
   return g == stream_grid(h, nb, ch, false) && stream_lds_fixed(h, g, nb, ch, true) <= kLdsBytes;
 }
 
-template <int FMT, int BITS, int NB, bool XST, int CH>
-hipError_t launch_stream_x(const qgemv_plan* p, const uint16_t* x, float* y, hipStream_t st) {
+template <int FMT, int BITS, int NB, bool XST, int CH, bool EPI>
+hipError_t launch_stream_x(const qgemv_plan* p, const uint16_t* x, float* y, const EpiArg<EPI>& ep, hipStream_t st) {
   constexpr int NR = 1;                // chunks in flight per wave
   const BlobHeader& h = p->h;
   const int grid = stream_grid(h, NB, CH, XST);
@@ -2058,21 +2160,21 @@ hipError_t launch_stream_x(const qgemv_plan* p, const uint16_t* x, float* y, hip
   // More than half of LDS keeps a second workgroup off the CU: one per CU.
   if (lds < kOneWorkgroupLds) lds = kOneWorkgroupLds;
   // once per instantiation (thread-safe static initialisation)
-  static const hipError_t attr = hipFuncSetAttribute((const void*)k_stream<FMT, BITS, CH, NR, NB, XST>,
+  static const hipError_t attr = hipFuncSetAttribute((const void*)k_stream<FMT, BITS, CH, NR, NB, XST, EPI>,
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLdsBytes);
   if (attr != hipSuccess) return attr;
   const uint32_t codes_bytes = (uint32_t)((uint64_t)h.tiles * h.nkb * h.block_bytes);
   const uint32_t meta_bytes = (uint32_t)(h.off_rowptr - h.off_meta);
-  hipLaunchKernelGGL((k_stream<FMT, BITS, CH, NR, NB, XST>), dim3(grid), dim3(64 * kWaves), lds, st, p->blob + h.off_codes,
+  hipLaunchKernelGGL((k_stream<FMT, BITS, CH, NR, NB, XST, EPI>), dim3(grid), dim3(64 * kWaves), lds, st, p->blob + h.off_codes,
                      (const uint32_t*)(p->blob + h.off_meta), (const int32_t*)(p->blob + h.off_rowptr),
                      (const uint32_t*)(p->blob + h.off_entries), (const int32_t*)(p->blob + h.off_boff),
                      (const uint32_t*)(p->blob + h.off_bent), x, y, h.M, h.K, h.Kp, h.nkb, h.tiles, codes_bytes,
-                     meta_bytes, (int)h.nnz, (int)(cap / 4), h.group_size > 0 ? h.group_size : 16);
+                     meta_bytes, (int)h.nnz, (int)(cap / 4), h.group_size > 0 ? h.group_size : 16, ep);
   return hipGetLastError();
 }
 
-template <int FMT, int BITS, int NB>
-hipError_t launch_stream(const qgemv_plan* p, const uint16_t* x, float* y, hipStream_t st) {
+template <int FMT, int BITS, int NB, bool EPI>
+hipError_t launch_stream(const qgemv_plan* p, const uint16_t* x, float* y, const EpiArg<EPI>& ep, hipStream_t st) {
   if constexpr (NB == 1) {
     // K-blocks per chunk at batch 1: single blocks when a workgroup holds one
     // tile (its 16 waves then share the tile's blocks more finely) and for
@@ -2080,11 +2182,11 @@ hipError_t launch_stream(const qgemv_plan* p, const uint16_t* x, float* y, hipSt
     // otherwise.
     const bool one = FMT == QGEMV_FMT_BPDQ || (p->h.tiles + stream_grid(p->h, 1, 2, false) - 1) /
                                                       stream_grid(p->h, 1, 2, false) <= 1;
-    return one ? launch_stream_x<FMT, BITS, NB, false, 1>(p, x, y, st)
-               : launch_stream_x<FMT, BITS, NB, false, 2>(p, x, y, st);
+    return one ? launch_stream_x<FMT, BITS, NB, false, 1, EPI>(p, x, y, ep, st)
+               : launch_stream_x<FMT, BITS, NB, false, 2, EPI>(p, x, y, ep, st);
   } else {
-    return stream_xst(p->h, NB, 3) ? launch_stream_x<FMT, BITS, NB, true, 3>(p, x, y, st)
-                                   : launch_stream_x<FMT, BITS, NB, false, 3>(p, x, y, st);
+    return stream_xst(p->h, NB, 3) ? launch_stream_x<FMT, BITS, NB, true, 3, EPI>(p, x, y, ep, st)
+                                   : launch_stream_x<FMT, BITS, NB, false, 3, EPI>(p, x, y, ep, st);
   }
 }
 
@@ -2112,8 +2214,8 @@ bool xlds_fits(const BlobHeader& h, int nb) {
   return h.tiles > xlds_grid(h) && xlds_fixed(h, xlds_grid(h), nb) + 1024 <= kLdsBytes;
 }
 
-template <int FMT, int BITS, int NB>
-hipError_t launch_xlds(const qgemv_plan* p, const uint16_t* x, float* y, hipStream_t st) {
+template <int FMT, int BITS, int NB, bool EPI>
+hipError_t launch_xlds(const qgemv_plan* p, const uint16_t* x, float* y, const EpiArg<EPI>& ep, hipStream_t st) {
   // code ring slots per wave: 4 for 4-bit codes (1 KiB per block), 3 for 3-bit
   constexpr int R = BITS == 4 ? 4 : 3;
   const BlobHeader& h = p->h;
@@ -2124,15 +2226,15 @@ hipError_t launch_xlds(const qgemv_plan* p, const uint16_t* x, float* y, hipStre
   cap &= ~(size_t)1023;  // whole 1 KiB wave copies
   size_t lds = fixed + cap;
   if (lds < kOneWorkgroupLds) lds = kOneWorkgroupLds;
-  static const hipError_t attr = hipFuncSetAttribute((const void*)k_xlds<FMT, BITS, NB, R>,
+  static const hipError_t attr = hipFuncSetAttribute((const void*)k_xlds<FMT, BITS, NB, R, EPI>,
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLdsBytes);
   if (attr != hipSuccess) return attr;
   const uint32_t codes_bytes = (uint32_t)((uint64_t)h.tiles * h.nkb * h.block_bytes);
   const uint32_t meta_bytes = (uint32_t)(h.off_rowptr - h.off_meta);
-  hipLaunchKernelGGL((k_xlds<FMT, BITS, NB, R>), dim3(grid), dim3(64 * kWaves), lds, st, p->blob + h.off_codes,
+  hipLaunchKernelGGL((k_xlds<FMT, BITS, NB, R, EPI>), dim3(grid), dim3(64 * kWaves), lds, st, p->blob + h.off_codes,
                      (const uint32_t*)(p->blob + h.off_meta), (const int32_t*)(p->blob + h.off_rowptr),
                      (const uint32_t*)(p->blob + h.off_entries), x, y, h.M, h.K, h.Kp, h.nkb, h.tiles, codes_bytes,
-                     meta_bytes, (int)h.nnz, (int)(cap / 4), h.group_size > 0 ? h.group_size : 16);
+                     meta_bytes, (int)h.nnz, (int)(cap / 4), h.group_size > 0 ? h.group_size : 16, ep);
   return hipGetLastError();
 }
 
@@ -2157,19 +2259,20 @@ bool pair_fits(const BlobHeader& h) {
   return h.format == QGEMV_FMT_LUT && h.bits == 4 && h.Kp <= 16384 && pair_lds(h, pair_grid(h)) <= kLdsBytes;
 }
 
-hipError_t launch_pair(const qgemv_plan* p, const uint16_t* x, float* y, hipStream_t st) {
+template <bool EPI>
+hipError_t launch_pair(const qgemv_plan* p, const uint16_t* x, float* y, const EpiArg<EPI>& ep, hipStream_t st) {
   constexpr int R = 4;  // code ring slots per wave
   const BlobHeader& h = p->h;
   const int grid = pair_grid(h);
   size_t lds = pair_lds(h, grid);
   if (lds < kOneWorkgroupLds) lds = kOneWorkgroupLds;
   static const hipError_t attr =
-      hipFuncSetAttribute((const void*)k_pair<R>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLdsBytes);
+      hipFuncSetAttribute((const void*)k_pair<R, EPI>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLdsBytes);
   if (attr != hipSuccess) return attr;
   const uint32_t meta_bytes = (uint32_t)(h.off_rowptr - h.off_meta);
-  hipLaunchKernelGGL((k_pair<R>), dim3(grid), dim3(64 * kWaves), lds, st, p->blob + h.off_codes,
+  hipLaunchKernelGGL((k_pair<R, EPI>), dim3(grid), dim3(64 * kWaves), lds, st, p->blob + h.off_codes,
                      (const uint32_t*)(p->blob + h.off_meta), (const int32_t*)(p->blob + h.off_rowptr),
-                     (const uint32_t*)(p->blob + h.off_entries), x, y, h.M, h.K, h.Kp, h.nkb, h.tiles, meta_bytes);
+                     (const uint32_t*)(p->blob + h.off_entries), x, y, h.M, h.K, h.Kp, h.nkb, h.tiles, meta_bytes, ep);
   return hipGetLastError();
 }
 
@@ -2225,30 +2328,30 @@ size_t split_ws_bytes(const BlobHeader& h, int nb, const SplitCfg& c) {
   return kSplitCtrBytes + (size_t)c.S * h.tiles * 16 * nb * 4;
 }
 
-template <int FMT, int BITS, int NB, int CH>
+template <int FMT, int BITS, int NB, int CH, bool EPI>
 hipError_t launch_split_ch(const qgemv_plan* p, const SplitCfg& c, const uint16_t* x, float* y, void* ws,
-                           hipStream_t st) {
+                           const EpiArg<EPI>& ep, hipStream_t st) {
   const BlobHeader& h = p->h;
-  static const hipError_t attr = hipFuncSetAttribute((const void*)k_split<FMT, BITS, NB, CH>,
+  static const hipError_t attr = hipFuncSetAttribute((const void*)k_split<FMT, BITS, NB, CH, EPI>,
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLdsBytes);
   if (attr != hipSuccess) return attr;
   const uint32_t codes_bytes = (uint32_t)((uint64_t)h.tiles * h.nkb * h.block_bytes);
   const uint32_t meta_bytes = (uint32_t)(h.off_rowptr - h.off_meta);
-  hipLaunchKernelGGL((k_split<FMT, BITS, NB, CH>), dim3(c.NG * c.S), dim3(64 * kWaves), c.lds, st,
+  hipLaunchKernelGGL((k_split<FMT, BITS, NB, CH, EPI>), dim3(c.NG * c.S), dim3(64 * kWaves), c.lds, st,
                      p->blob + h.off_codes, (const uint32_t*)(p->blob + h.off_meta),
                      (const int32_t*)(p->blob + h.off_boff), (const uint32_t*)(p->blob + h.off_bent), x, y,
                      (float*)((uint8_t*)ws + kSplitCtrBytes), (uint32_t*)ws, h.M, h.K, h.nkb, h.tiles, codes_bytes,
-                     meta_bytes, (int)h.nnz, h.group_size > 0 ? h.group_size : 16, c.S, c.NG);
+                     meta_bytes, (int)h.nnz, h.group_size > 0 ? h.group_size : 16, c.S, c.NG, ep);
   return hipGetLastError();
 }
 
-template <int FMT, int BITS, int NB>
+template <int FMT, int BITS, int NB, bool EPI>
 hipError_t launch_split(const qgemv_plan* p, const SplitCfg& c, const uint16_t* x, float* y, void* ws,
-                        hipStream_t st) {
-  if (c.CH == 1) return launch_split_ch<FMT, BITS, NB, 1>(p, c, x, y, ws, st);
-  return c.CH == 2   ? launch_split_ch<FMT, BITS, NB, 2>(p, c, x, y, ws, st)
-         : c.CH == 4 ? launch_split_ch<FMT, BITS, NB, 4>(p, c, x, y, ws, st)
-                     : launch_split_ch<FMT, BITS, NB, 8>(p, c, x, y, ws, st);
+                        const EpiArg<EPI>& ep, hipStream_t st) {
+  if (c.CH == 1) return launch_split_ch<FMT, BITS, NB, 1, EPI>(p, c, x, y, ws, ep, st);
+  return c.CH == 2   ? launch_split_ch<FMT, BITS, NB, 2, EPI>(p, c, x, y, ws, ep, st)
+         : c.CH == 4 ? launch_split_ch<FMT, BITS, NB, 4, EPI>(p, c, x, y, ws, ep, st)
+                     : launch_split_ch<FMT, BITS, NB, 8, EPI>(p, c, x, y, ws, ep, st);
 }
 
 // HPTQ: one workgroup per CU over its tile range; G = 3 blocks decoded side
@@ -2256,24 +2359,24 @@ hipError_t launch_split(const qgemv_plan* p, const SplitCfg& c, const uint16_t* 
 // without spilling, else fewer.  Long codewords
 // go through the second-level tables where they fit in LDS, else through the
 // canonical search.  x sits in LDS at batch 1 and is read from L2 at 8/16.
-template <int G, bool SUB, int NB>
+template <int G, bool SUB, int NB, bool EPI>
 hipError_t launch_huff_g(const qgemv_plan* p, const uint16_t* x, float* y, int grid, size_t lds, int bufw,
-                         hipStream_t st) {
+                         const EpiArg<EPI>& ep, hipStream_t st) {
   const BlobHeader& h = p->h;
   static const hipError_t attr =
-      hipFuncSetAttribute((const void*)k_huff<G, SUB, NB>, hipFuncAttributeMaxDynamicSharedMemorySize,
+      hipFuncSetAttribute((const void*)k_huff<G, SUB, NB, EPI>, hipFuncAttributeMaxDynamicSharedMemorySize,
                           (int)(kLdsBytes - (size_t)kHuffTable * 64 * 4 - 64));
   if (attr != hipSuccess) return attr;
-  hipLaunchKernelGGL((k_huff<G, SUB, NB>), dim3(grid), dim3(64 * kWaves), lds, st,
+  hipLaunchKernelGGL((k_huff<G, SUB, NB, EPI>), dim3(grid), dim3(64 * kWaves), lds, st,
                      (const uint32_t*)(p->blob + h.off_codes), (const uint16_t*)(p->blob + h.off_meta),
                      (const uint32_t*)(p->blob + h.off_hidx), (const uint16_t*)(p->blob + h.off_hlane),
                      (const int32_t*)(p->blob + h.off_htab), (const int16_t*)(p->blob + h.off_hsym), x, y, h.M, h.K,
-                     h.nkb, h.tiles, h.hsym, h.hwords, bufw, (int)h.hsub);
+                     h.nkb, h.tiles, h.hsym, h.hwords, bufw, (int)h.hsub, ep);
   return hipGetLastError();
 }
 
-template <int NB>
-hipError_t launch_huff_nb(const qgemv_plan* p, const uint16_t* x, float* y, hipStream_t st) {
+template <int NB, bool EPI>
+hipError_t launch_huff_nb(const qgemv_plan* p, const uint16_t* x, float* y, const EpiArg<EPI>& ep, hipStream_t st) {
   const BlobHeader& h = p->h;
   const int grid = h.tiles < kMaxGrid ? h.tiles : kMaxGrid;
   const size_t tw = (size_t)((h.tiles + grid - 1) / grid);
@@ -2292,41 +2395,47 @@ hipError_t launch_huff_nb(const qgemv_plan* p, const uint16_t* x, float* y, hipS
       if (lds + table < kOneWorkgroupLds) lds = kOneWorkgroupLds - table;
       if (g == 3) {
         if constexpr (NB == 1)
-          return sub ? launch_huff_g<3, true, NB>(p, x, y, grid, lds, bufw, st)
-                     : launch_huff_g<3, false, NB>(p, x, y, grid, lds, bufw, st);
+          return sub ? launch_huff_g<3, true, NB, EPI>(p, x, y, grid, lds, bufw, ep, st)
+                     : launch_huff_g<3, false, NB, EPI>(p, x, y, grid, lds, bufw, ep, st);
         else if constexpr (NB == 8)
-          return launch_huff_g<3, true, NB>(p, x, y, grid, lds, bufw, st);
+          return launch_huff_g<3, true, NB, EPI>(p, x, y, grid, lds, bufw, ep, st);
       }
       if (sub)
-        return g == 2 ? launch_huff_g<2, true, NB>(p, x, y, grid, lds, bufw, st)
-                      : launch_huff_g<1, true, NB>(p, x, y, grid, lds, bufw, st);
-      return g == 2 ? launch_huff_g<2, false, NB>(p, x, y, grid, lds, bufw, st)
-                    : launch_huff_g<1, false, NB>(p, x, y, grid, lds, bufw, st);
+        return g == 2 ? launch_huff_g<2, true, NB, EPI>(p, x, y, grid, lds, bufw, ep, st)
+                      : launch_huff_g<1, true, NB, EPI>(p, x, y, grid, lds, bufw, ep, st);
+      return g == 2 ? launch_huff_g<2, false, NB, EPI>(p, x, y, grid, lds, bufw, ep, st)
+                    : launch_huff_g<1, false, NB, EPI>(p, x, y, grid, lds, bufw, ep, st);
     }
   }
   return hipErrorInvalidValue;
 }
 
-hipError_t launch_huff(const qgemv_plan* p, const uint16_t* x, float* y, int batch, hipStream_t st) {
-  return batch == 1   ? launch_huff_nb<1>(p, x, y, st)
-         : batch == 8 ? launch_huff_nb<8>(p, x, y, st)
-                      : launch_huff_nb<16>(p, x, y, st);
+template <bool EPI>
+hipError_t launch_huff(const qgemv_plan* p, const uint16_t* x, float* y, int batch, const EpiArg<EPI>& ep,
+                       hipStream_t st) {
+  return batch == 1   ? launch_huff_nb<1, EPI>(p, x, y, ep, st)
+         : batch == 8 ? launch_huff_nb<8, EPI>(p, x, y, ep, st)
+                      : launch_huff_nb<16, EPI>(p, x, y, ep, st);
 }
 
 // ws: the K-split workspace for this batch (split_ws_bytes), or null to use
 // the kernels that need none.
-template <int FMT, int BITS>
-hipError_t launch_run(const qgemv_plan* p, const uint16_t* x, float* y, int batch, void* ws, hipStream_t st) {
+template <int FMT, int BITS, bool EPI>
+hipError_t launch_run(const qgemv_plan* p, const uint16_t* x, float* y, int batch, void* ws, const EpiArg<EPI>& ep,
+                      hipStream_t st) {
   if (batch == 1) {
-    if (FMT == QGEMV_FMT_LUT && BITS == 4 && pair_fits(p->h)) return launch_pair(p, x, y, st);
-    return launch_stream<FMT, BITS, 1>(p, x, y, st);
+    if (FMT == QGEMV_FMT_LUT && BITS == 4 && pair_fits(p->h)) return launch_pair<EPI>(p, x, y, ep, st);
+    return launch_stream<FMT, BITS, 1, EPI>(p, x, y, ep, st);
   }
   SplitCfg c;
   if (ws && split_config(p->h, batch, c))
-    return batch == 8 ? launch_split<FMT, BITS, 8>(p, c, x, y, ws, st) : launch_split<FMT, BITS, 16>(p, c, x, y, ws, st);
+    return batch == 8 ? launch_split<FMT, BITS, 8, EPI>(p, c, x, y, ws, ep, st)
+                      : launch_split<FMT, BITS, 16, EPI>(p, c, x, y, ws, ep, st);
   if (batch == 8)
-    return xlds_fits(p->h, 8) ? launch_xlds<FMT, BITS, 8>(p, x, y, st) : launch_stream<FMT, BITS, 8>(p, x, y, st);
-  return xlds_fits(p->h, 16) ? launch_xlds<FMT, BITS, 16>(p, x, y, st) : launch_stream<FMT, BITS, 16>(p, x, y, st);
+    return xlds_fits(p->h, 8) ? launch_xlds<FMT, BITS, 8, EPI>(p, x, y, ep, st)
+                              : launch_stream<FMT, BITS, 8, EPI>(p, x, y, ep, st);
+  return xlds_fits(p->h, 16) ? launch_xlds<FMT, BITS, 16, EPI>(p, x, y, ep, st)
+                             : launch_stream<FMT, BITS, 16, EPI>(p, x, y, ep, st);
 }
 
 template <int FMT, int BITS>
@@ -2417,6 +2526,33 @@ int plan_workspace(qgemv_plan* p, hipStream_t st, void** ws) {
   return QGEMV_OK;
 }
 
+// Check an epilogue against the plan and fill the kernels' argument.
+int epilogue_arg(const qgemv_plan* p, void* y, int batch, const qgemv_epilogue* e, EpiArg<true>& a) {
+  if (!e) return QGEMV_ERR_INVALID_ARG;
+  if (batch != 1 && batch != 8 && batch != 16) return QGEMV_ERR_UNSUPPORTED;
+  if (e->act < QGEMV_ACT_NONE || e->act > QGEMV_ACT_SILU) return QGEMV_ERR_UNSUPPORTED;
+  for (int t : {e->y_type, e->bias_type, e->residual_type})
+    if (t != QGEMV_F16 && t != QGEMV_F32) return QGEMV_ERR_UNSUPPORTED;
+  if (e->gated && p->h.M % 2) return QGEMV_ERR_UNSUPPORTED;
+  const int64_t mo = e->gated ? p->h.M / 2 : p->h.M;
+  const int64_t ldy = e->ldy ? e->ldy : mo, ldr = e->ldr ? e->ldr : mo;
+  if (ldy < mo || ldr < mo) return QGEMV_ERR_INVALID_ARG;
+  auto misaligned = [](const void* q, int t) { return (uintptr_t)q % (t == QGEMV_F32 ? 4 : 2) != 0; };
+  if (misaligned(y, e->y_type) || misaligned(e->bias, e->bias_type) || misaligned(e->residual, e->residual_type))
+    return QGEMV_ERR_INVALID_ARG;
+  a.bias = e->bias;
+  a.residual = e->residual;
+  a.y = y;
+  a.ldy = ldy;
+  a.ldr = ldr;
+  a.act = e->act;
+  a.gated = e->gated != 0;
+  a.y32 = e->y_type == QGEMV_F32;
+  a.bias32 = e->bias_type == QGEMV_F32;
+  a.res32 = e->residual_type == QGEMV_F32;
+  return QGEMV_OK;
+}
+
 // Device address of `scratch` on device dev, looked up once per device with
 // that device current.
 constexpr int kMaxDevices = 64;
@@ -2443,14 +2579,17 @@ int scratch_address(int dev, void** out) {
   return QGEMV_OK;
 }
 
-hipError_t launch_format(const qgemv_plan* p, const uint16_t* x, float* y, int batch, void* ws, hipStream_t st) {
+template <bool EPI>
+hipError_t launch_format(const qgemv_plan* p, const uint16_t* x, float* y, int batch, void* ws, const EpiArg<EPI>& ep,
+                         hipStream_t st) {
   const bool b4 = p->h.bits == 4;
-  if (p->h.format == QGEMV_FMT_HPTQ) return launch_huff(p, x, y, batch, st);
+  if (p->h.format == QGEMV_FMT_HPTQ) return launch_huff<EPI>(p, x, y, batch, ep, st);
   if (p->h.format == QGEMV_FMT_LUT)
-    return b4 ? launch_run<QGEMV_FMT_LUT, 4>(p, x, y, batch, ws, st) : launch_run<QGEMV_FMT_LUT, 3>(p, x, y, batch, ws, st);
-  if (p->h.format == QGEMV_FMT_BPDQ) return launch_run<QGEMV_FMT_BPDQ, 3>(p, x, y, batch, ws, st);
-  return b4 ? launch_run<QGEMV_FMT_UNIFORM, 4>(p, x, y, batch, ws, st)
-            : launch_run<QGEMV_FMT_UNIFORM, 3>(p, x, y, batch, ws, st);
+    return b4 ? launch_run<QGEMV_FMT_LUT, 4, EPI>(p, x, y, batch, ws, ep, st)
+              : launch_run<QGEMV_FMT_LUT, 3, EPI>(p, x, y, batch, ws, ep, st);
+  if (p->h.format == QGEMV_FMT_BPDQ) return launch_run<QGEMV_FMT_BPDQ, 3, EPI>(p, x, y, batch, ws, ep, st);
+  return b4 ? launch_run<QGEMV_FMT_UNIFORM, 4, EPI>(p, x, y, batch, ws, ep, st)
+            : launch_run<QGEMV_FMT_UNIFORM, 3, EPI>(p, x, y, batch, ws, ep, st);
 }
 
 }  // namespace
@@ -2497,7 +2636,7 @@ int qgemv_run(qgemv_handle h, const void* x_dev, float* y_dev, int32_t batch, vo
     const int stw = plan_workspace(h, st, &ws);
     if (stw != QGEMV_OK) return stw;
   }
-  return hip_status(launch_format(h, (const uint16_t*)x_dev, y_dev, batch, ws, st));
+  return hip_status(launch_format<false>(h, (const uint16_t*)x_dev, y_dev, batch, ws, {}, st));
 }
 
 int qgemv_run_noalloc(qgemv_handle h, const void* x_dev, float* y_dev, int32_t batch, void* stream) {
@@ -2511,7 +2650,23 @@ int qgemv_run_noalloc(qgemv_handle h, const void* x_dev, float* y_dev, int32_t b
     const int sts = scratch_address(h->device, &ws);
     if (sts != QGEMV_OK) return sts;
   }
-  return hip_status(launch_format(h, (const uint16_t*)x_dev, y_dev, batch, ws, (hipStream_t)stream));
+  return hip_status(launch_format<false>(h, (const uint16_t*)x_dev, y_dev, batch, ws, {}, (hipStream_t)stream));
+}
+
+int qgemv_run_epilogue(qgemv_handle h, const void* x_dev, void* y_dev, int32_t batch, const qgemv_epilogue* e,
+                       void* stream) {
+  if (!h || !x_dev || !y_dev) return QGEMV_ERR_INVALID_ARG;
+  EpiArg<true> ep;
+  const int ste = epilogue_arg(h, y_dev, batch, e, ep);
+  if (ste != QGEMV_OK) return ste;
+  if ((uintptr_t)x_dev % 16) return QGEMV_ERR_INVALID_ARG;
+  const hipStream_t st = (hipStream_t)stream;
+  void* ws = nullptr;
+  if (batch > 1) {
+    const int stw = plan_workspace(h, st, &ws);
+    if (stw != QGEMV_OK) return stw;
+  }
+  return hip_status(launch_format<true>(h, (const uint16_t*)x_dev, nullptr, batch, ws, ep, st));
 }
 
 int qgemv_debug_unpack(qgemv_handle h, uint8_t* codes_dev, void* stream) {

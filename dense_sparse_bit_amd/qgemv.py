@@ -27,6 +27,7 @@ LIB_PATH = os.path.join(HERE, "libdsb_qgemv.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "qgemv.h")
 
 FMT = {"uniform": 0, "lut": 1, "bpdq": 2, "hptq": 3}
+ACT = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 STATUS = {0: "QGEMV_OK", -1: "QGEMV_ERR_INVALID_ARG", -2: "QGEMV_ERR_MALFORMED_CSR",
           -3: "QGEMV_ERR_UNSUPPORTED", -4: "QGEMV_ERR_HIP", -5: "QGEMV_ERR_SIZE", -6: "QGEMV_ERR_SCRATCH"}
 
@@ -59,6 +60,15 @@ class Weights(ctypes.Structure):
     ]
 
 
+class Epilogue(ctypes.Structure):
+    """qgemv_epilogue of include/qgemv_epilogue.h."""
+    _fields_ = [
+        ("act", ctypes.c_int32), ("gated", ctypes.c_int32), ("y_type", ctypes.c_int32),
+        ("bias_type", ctypes.c_int32), ("residual_type", ctypes.c_int32),
+        ("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("ldr", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
@@ -78,6 +88,8 @@ def lib() -> ctypes.CDLL:
     L.qgemv_run.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]
     L.qgemv_run_noalloc.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
                                      ctypes.c_void_p]
+    L.qgemv_run_epilogue.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                     ctypes.POINTER(Epilogue), ctypes.c_void_p]
     L.qgemv_debug_unpack.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
     L.qgemv_destroy.argtypes = [ctypes.c_void_p]
     L.qgemv_read_probe.argtypes = [ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]
@@ -85,10 +97,35 @@ def lib() -> ctypes.CDLL:
     L.qgemv_error_string.restype = ctypes.c_char_p
     L.qgemv_last_hip_error.argtypes = []
     for f in ("qgemv_packed_size", "qgemv_repack", "qgemv_unpack_host", "qgemv_create", "qgemv_run", "qgemv_run_noalloc",
-              "qgemv_debug_unpack", "qgemv_read_probe", "qgemv_destroy", "qgemv_last_hip_error"):
+              "qgemv_run_epilogue", "qgemv_debug_unpack", "qgemv_read_probe", "qgemv_destroy", "qgemv_last_hip_error"):
         getattr(L, f).restype = ctypes.c_int
     _lib = L
     return L
+
+
+class _launch:
+    """The HIP stream to launch on, with `dev` current and, if a stream is given, that stream current too
+    (so that what is allocated inside belongs to it).  Does nothing where both already hold."""
+
+    def __init__(self, dev, stream):
+        self.dev, self.stream, self.ctx = dev, stream, None
+
+    def __enter__(self):
+        import torch
+        if self.stream is not None:
+            if self.stream.device != self.dev:
+                raise ValueError(f"the stream must be on the device {self.dev}")
+            self.ctx = torch.cuda.stream(self.stream)
+        elif self.dev.index is not None and torch.cuda.current_device() != self.dev.index:
+            self.ctx = torch.cuda.device(self.dev)
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return (self.stream or torch.cuda.current_stream(self.dev)).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+        return False
 
 
 def header_symbols() -> list:
@@ -165,6 +202,43 @@ def unpack_host(blob: np.ndarray, M: int, K: int) -> np.ndarray:
     return out
 
 
+def interleave_rows(gate: dict, up: dict) -> dict:
+    """One weight set whose rows 2i and 2i + 1 are row i of gate and row i of up
+    (canonical arrays of equal shape, format, code width and group): the weights
+    of a gated product.  Every part of these formats is per row; an HPTQ stream
+    has one code for all rows, so two of them cannot be joined this way."""
+    fmt = gate["fmt"]
+    if fmt == "hptq" or up["fmt"] != fmt:
+        raise ValueError("gate and up must share one of the formats uniform, lut, bpdq")
+    for key in ("M", "K", "bits"):
+        if gate[key] != up[key]:
+            raise ValueError(f"gate and up differ in {key}")
+    if fmt == "bpdq" and gate["group"] != up["group"]:
+        raise ValueError("gate and up differ in group")
+    out = {k: gate[k] for k in ("K", "bits", "fmt")}
+    out["group"] = gate.get("group", 0)
+    M = int(gate["M"])
+    out["M"] = 2 * M
+    for key in ("codes_packed", "scales", "zeros", "lut", "coefs"):
+        if gate.get(key) is not None:
+            a, b = np.asarray(gate[key]), np.asarray(up[key])
+            out[key] = np.stack([a, b], axis=1).reshape((2 * M,) + a.shape[1:])
+    counts = np.stack([np.diff(np.asarray(w["row_ptr"], dtype=np.int64)) for w in (gate, up)], axis=1).ravel()
+    row_ptr = np.concatenate([[0], np.cumsum(counts)])
+    out["row_ptr"] = row_ptr.astype(np.int32)
+    col = np.zeros(int(row_ptr[-1]), dtype=np.int32)
+    val = np.zeros(int(row_ptr[-1]), dtype=np.float16)
+    for odd, w in enumerate((gate, up)):
+        n = np.diff(np.asarray(w["row_ptr"], dtype=np.int64))
+        # entry p of source row i goes to the start of row 2i + odd, plus p's place in its row
+        at = np.repeat(row_ptr[odd:2 * M:2] - np.asarray(w["row_ptr"], dtype=np.int64)[:-1], n) + np.arange(int(n.sum()))
+        if len(at):
+            col[at] = np.asarray(w["col_idx"])
+            val[at] = np.asarray(w["values"]).view(np.float16)
+    out["col_idx"], out["values"] = col, val
+    return out
+
+
 class QGemv:
     """A plan bound to one weight set in device memory (owned by a torch tensor)."""
 
@@ -211,6 +285,57 @@ class QGemv:
         s = (stream or torch.cuda.current_stream(x.device)).cuda_stream
         _check(lib().qgemv_run_noalloc(self._h, x.data_ptr(), y.data_ptr(), B, s), "qgemv_run_noalloc")
         return y
+
+    def run_epilogue(self, x, bias=None, act="none", gated=False, residual=None, out=None, dtype=None, stream=None):
+        """act(W x + bias) + residual, or with gated (rows 2i, 2i + 1 = gate, up; see interleave_rows)
+        act(gate) * up + residual; returns out [B, M] ([B, M // 2] gated).
+
+        x: FP16 [B, K], contiguous, B in {1, 8, 16}.  bias [M] and residual [B, M or M // 2]: FP16 or fp32.
+        act: "none", "relu", "gelu", "gelu_tanh" or "silu".  out: FP16 or fp32, allocated as dtype (FP16 by
+        default) if not given; out and residual may be rows of wider arrays, and residual may be out itself.
+        All on the plan's device; stream: as run().  With uniform codes at B 8 or 16 runs of one plan share its
+        workspace and must not overlap, and the first must not be captured into a graph.
+        """
+        import torch
+        dev = self.blob.device
+        f16, f32 = torch.float16, torch.float32
+        if x.dim() == 1:
+            x = x.unsqueeze(0)
+        if x.dim() != 2 or x.dtype != f16 or not x.is_contiguous() or x.shape[1] != self.K:
+            raise ValueError("x must be a contiguous FP16 [B, K] tensor")
+        if act not in ACT:
+            raise ValueError(f"act must be one of {sorted(ACT)}")
+        B = x.shape[0]
+        mo = self.M // 2 if gated else self.M
+        e = Epilogue()
+        e.act, e.gated = ACT[act], bool(gated)
+        if bias is not None:
+            if bias.dtype not in (f16, f32) or not bias.is_contiguous() or tuple(bias.shape) != (self.M,):
+                raise ValueError("bias must be a contiguous FP16 or fp32 [M] tensor")
+            e.bias, e.bias_type = bias.data_ptr(), int(bias.dtype == f32)
+        if residual is not None:
+            if residual.dtype not in (f16, f32) or tuple(residual.shape) != (B, mo) or residual.stride(1) != 1 or (
+                    B > 1 and residual.stride(0) < mo):
+                raise ValueError("residual must be an FP16 or fp32 [B, outputs] tensor with contiguous rows")
+            e.residual, e.residual_type = residual.data_ptr(), int(residual.dtype == f32)
+            e.ldr = residual.stride(0) if B > 1 else 0
+        if out is not None:
+            if out.dtype not in (f16, f32) or tuple(out.shape) != (B, mo) or out.stride(1) != 1 or (
+                    B > 1 and out.stride(0) < mo) or (dtype is not None and dtype != out.dtype):
+                raise ValueError("out must be an FP16 or fp32 [B, outputs] tensor with contiguous rows")
+            e.ldy = out.stride(0) if B > 1 else 0
+        elif dtype not in (None, f16, f32):
+            raise ValueError("dtype must be torch.float16 or torch.float32")
+        for t in (x, bias, residual, out):
+            if t is not None and t.device != dev:
+                raise ValueError(f"all tensors must be on the plan's device {dev}")
+        with _launch(dev, stream) as s:
+            if out is None:
+                out = torch.empty((B, mo), dtype=dtype or f16, device=dev)
+            e.y_type = int(out.dtype == f32)
+            _check(lib().qgemv_run_epilogue(self._h, x.data_ptr(), out.data_ptr(), B, ctypes.byref(e), s),
+                   "qgemv_run_epilogue")
+        return out
 
     def debug_unpack(self, stream=None):
         import torch
