@@ -14,7 +14,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdsb_qgemv.so")
-SOURCES = ["qgemv_kernels.hip", "qgemv_host.cpp"]
+SOURCES = ["qgemv_kernels.hip", "qcache_kernels.hip", "qgemv_host.cpp"]
 ARCH = "gfx950"
 
 FLAGS = [
