@@ -5,6 +5,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/qcache.h"
 #include "qcache_layout.h"
@@ -259,10 +260,14 @@ k_qcache_read(const uint8_t* __restrict__ cache, Seqs sq, Rows k, Rows v, int he
 // [64, 128): sums over a group stay in FP16's range, and q / 16 is exact down
 // to 2^-20 of the largest element.
 //
+// A wave's next 32 positions are copied from HBM straight into its own part of
+// LDS while it works on the current ones, which it holds in registers; the
+// units' statistics, which 4 or 16 lanes share, then cross HBM once.
+//
 // At the end of an item's blocks the four waves' (m, sum, O) meet in LDS.  An
 // item that lies in one workgroup's range is finished there; otherwise each
-// workgroup leaves a partial (at most two per workgroup: the item it starts in
-// and the one it ends in), and k_qcache_join adds an item's partials in order.
+// workgroup leaves a partial (at most two per workgroup: the item it starts in,
+// slot 0, and the one it ends in, slot 1), and k_qcache_join adds them in order.
 // ---------------------------------------------------------------------------
 struct AttendArgs {
   Seqs sq;
@@ -270,8 +275,9 @@ struct AttendArgs {
   const uint16_t* q;
   uint16_t* out;
   int64_t q_ts, q_hs, o_ts, o_hs;
-  float* ws_ml;  // [grid][2][rows][2]: m, sum
   float* ws_o;   // [grid][2][rows][D]
+  float* ws_ml;  // [grid][2][rows][2]: m (log2), sum
+  int* ws_join;  // [grid][4]: last workgroup of the item that this one ends in (-1: none), its first row, item, rows
   int heads, per, rows, grid;
   float scale2;  // scale * log2 e
 };
@@ -290,14 +296,17 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int s) {
   return w;
 }
 
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
 __device__ __forceinline__ int wave_scan(int v) {  // inclusive
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
-  return v;
+  v = dpp_add<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8: inside the rows of 16
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);  // lane 15 of rows 0, 2 to rows 1, 3
+  return dpp_add<0x143, 0xC>(v);  // lane 31 to rows 2, 3
 }
 
 __device__ __forceinline__ float column_max(float v) {  // over the four lanes of a column
@@ -309,157 +318,326 @@ __device__ __forceinline__ float column_sum(float v) {
   return v + __shfl_xor(v, 32);
 }
 
-__device__ __forceinline__ uint32_t pk_h(float a, float b) { return (uint32_t)f2h(a) | ((uint32_t)f2h(b) << 16); }
+typedef float floatx2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pk_h(float a, float b) {  // round to nearest even
+  return as_u32(__builtin_convertvector((floatx2_t){a, b}, half2_t));
+}
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }  // 1 ulp; results below 2^-126 are 0
 
-// What a lane loads of one unit.
+// The same value, unknown to the compiler: what is computed from it stays where it is written, instead of being
+// kept in registers across a loop that has none to spare.
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// (w & mask) | magic in one instruction
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
+  uint32_t d;
+  asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(d) : "v"(w), "s"(mask), "v"(magic));
+  return d;
+}
+
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+constexpr int kNonTemporal = 2;
+
+// Copy `bytes` (a multiple of 16, the same for all lanes) from src to LDS, 16 bytes a lane and round; with no source, zeros.
+template <int BYTES>
+__device__ __forceinline__ void copy_to_lds(const uint8_t* src, bool real, uint8_t* dst, int lane) {
+  const rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(src), (short)0, real ? BYTES : 0, 0x00020000);
+#pragma unroll
+  for (int o = 0; o < BYTES; o += 1024)
+    if (o + 1024 <= BYTES || o + 16 * lane < BYTES)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)(dst + o), 16, 16 * lane, o, 0,
+                                               kNonTemporal);
+}
+
+// What a lane holds of one unit: the keys' part, and the values' part.
 template <int D, int NG>
-struct UnitRegs {
-  uint32_t k[D / 32], v[D / 32], ks[2 * NG], kl[(NG + 1) / 2], vs[4];
+struct KeyRegs {
+  uint32_t k[D / 32], ks[2 * NG], kl[(NG + 1) / 2];
+};
+template <int D>
+struct ValueRegs {
+  uint32_t v[D / 32], vs[4];
 };
 
 template <int N>
-__device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t* d) {
+__device__ __forceinline__ void read_dwords(const uint8_t* p, uint32_t* d) {
   if constexpr (N == 1) {
-    d[0] = __builtin_nontemporal_load((const uint32_t*)p);
+    d[0] = *(const uint32_t*)p;
   } else if constexpr (N == 2) {
-    const u32x2_t x = __builtin_nontemporal_load((const u32x2_t*)p);
+    const u32x2_t x = *(const u32x2_t*)p;
     d[0] = x[0], d[1] = x[1];
   } else {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-      const u32x4_t x = __builtin_nontemporal_load((const u32x4_t*)p + i / 4);
+      const u32x4_t x = ((const u32x4_t*)p)[i / 4];
       d[i] = x[0], d[i + 1] = x[1], d[i + 2] = x[2], d[i + 3] = x[3];
     }
   }
 }
 
 template <int D, int NG>
-__device__ __forceinline__ void load_unit(const uint8_t* unit, int lane, UnitRegs<D, NG>& r) {
+__device__ __forceinline__ void read_keys(const uint8_t* unit, int lane, KeyRegs<D, NG>& r) {
   using L = Geo<D, NG>;
   const int n = lane & 15, kq = lane >> 4;
-  load_dwords<L::ND>(unit + lane * (4 * L::ND), r.k);
-  load_dwords<L::ND>(unit + L::off_v + lane * (4 * L::ND), r.v);
-  load_dwords<2 * NG>(unit + L::off_ks + kq * (8 * NG), r.ks);
+  read_dwords<L::ND>(unit + lane * (4 * L::ND), r.k);
+  read_dwords<2 * NG>(unit + L::off_ks + kq * (8 * NG), r.ks);
   if constexpr (NG == 1) r.kl[0] = ((const uint16_t*)(unit + L::off_kl))[n];
-  else load_dwords<NG / 2>(unit + L::off_kl + n * (2 * NG), r.kl);
-  load_dwords<4>(unit + L::off_vs + (kq * NG + n * (D / 16) / L::G) * 16, r.vs);
+  else read_dwords<NG / 2>(unit + L::off_kl + n * (2 * NG), r.kl);
 }
 
-// Scores of a unit: st[i] = token 4 kq + i against column n, in log2 units.
+// The values' part of a tile's two units.  Written out, with the wait in the
+// same block, because the next tile's copy into LDS is then under way: the
+// compiler, not knowing which bytes it writes, would wait for it before any LDS
+// read of its own.
 template <int D, int NG>
-__device__ __forceinline__ void unit_scores(const UnitRegs<D, NG>& r, const u32x4_t (&qf)[D / 32], u32x4_t qs,
-                                            float k_s, float k_l, float (&st)[4]) {
+__device__ __forceinline__ void read_values(const uint8_t* tile, int lane, ValueRegs<D> (&r)[2]) {
+  using L = Geo<D, NG>;
+  const int n = lane & 15, kq = lane >> 4;
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)tile;
+  const uint32_t av = at + L::off_v + (uint32_t)lane * (4 * L::ND);
+  const uint32_t as = at + L::off_vs + (uint32_t)(kq * NG + n * (D / 16) / L::G) * 16;
+  u32x4_t s0, s1;
+  if constexpr (L::ND == 2) {
+    u32x2_t v0, v1;
+    asm volatile(
+        "ds_read_b64 %0, %4\n\tds_read_b64 %1, %4 offset:%6\n\tds_read_b128 %2, %5\n\tds_read_b128 %3, %5 offset:%6\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v0), "=&v"(v1), "=&v"(s0), "=&v"(s1)
+        : "v"(av), "v"(as), "n"(L::bytes)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r[0].v[i] = v0[i], r[1].v[i] = v1[i];
+  } else if constexpr (L::ND == 4) {
+    u32x4_t v0, v1;
+    asm volatile(
+        "ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:%6\n\tds_read_b128 %2, %5\n\tds_read_b128 %3, %5 offset:%6\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v0), "=&v"(v1), "=&v"(s0), "=&v"(s1)
+        : "v"(av), "v"(as), "n"(L::bytes)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[0].v[i] = v0[i], r[1].v[i] = v1[i];
+  } else {
+    u32x4_t v0, v1, v2, v3;
+    asm volatile(
+        "ds_read_b128 %0, %6\n\tds_read_b128 %1, %6 offset:16\n\tds_read_b128 %2, %6 offset:%8\n\t"
+        "ds_read_b128 %3, %6 offset:%9\n\tds_read_b128 %4, %7\n\tds_read_b128 %5, %7 offset:%8\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v0), "=&v"(v1), "=&v"(v2), "=&v"(v3), "=&v"(s0), "=&v"(s1)
+        : "v"(av), "v"(as), "n"(L::bytes), "n"(L::bytes + 16)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[0].v[i] = v0[i], r[0].v[4 + i] = v1[i], r[1].v[i] = v2[i], r[1].v[4 + i] = v3[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[0].vs[i] = s0[i], r[1].vs[i] = s1[i];
+}
+
+// Scores of a tile: st[e][i] = token 4 kq + i of unit e against column n, in units of the column's k_l.
+// The scheduling barriers keep one group's operands in registers at a time: left to itself the compiler
+// unpacks all of them first, and the kernel spills.
+template <int D, int NG>
+__device__ __forceinline__ void tile_scores(const KeyRegs<D, NG> (&r)[2], const u32x4_t (&qf)[D / 32], u32x4_t qs,
+                                            float (&st)[2][4]) {
   using L = Geo<D, NG>;
   const floatx4_t zero = {0.f, 0.f, 0.f, 0.f};
-  float t[4] = {0.f, 0.f, 0.f, 0.f};
+  floatx4_t acc[2];
+  float t[2][4];
+  auto scale = [&](int g) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float step = h2f((uint16_t)(r[e].ks[2 * g + i / 2] >> (16 * (i & 1))));
+        t[e][i] = g == 0 ? step * acc[e][i] : step * acc[e][i] + t[e][i];
+      }
+  };
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
-    floatx4_t acc = zero;
+    floatx4_t nxt[2] = {zero, zero};
 #pragma unroll
-    for (int j = g * (L::G / 32); j < (g + 1) * (L::G / 32); ++j) {
-      const uint32_t w = r.k[j], w8 = w >> 8;
-      acc = mfma((u32x4_t){w & 0x000F000Fu, w & 0x00F000F0u, w8 & 0x000F000Fu, w8 & 0x00F000F0u}, qf[j], acc);
-    }
+    for (int j = g * (L::G / 32); j < (g + 1) * (L::G / 32); ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      t[i] = h2f((uint16_t)(r.ks[2 * g + i / 2] >> (16 * (i & 1)))) * acc[i] + t[i];
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t w = r[e].k[j], w8 = w >> 8;
+        nxt[e] = mfma((u32x4_t){w & 0x000F000Fu, w & 0x00F000F0u, w8 & 0x000F000Fu, w8 & 0x00F000F0u}, qf[j], nxt[e]);
+      }
+    if (g > 0) scale(g - 1);
+    acc[0] = nxt[0];
+    acc[1] = nxt[1];
+    __builtin_amdgcn_sched_barrier(0);
   }
-  u32x4_t lo = {0u, 0u, 0u, 0u};
+  floatx4_t la[2];
 #pragma unroll
-  for (int i = 0; i < (NG + 1) / 2; ++i) lo[i] = r.kl[i];
-  const floatx4_t la = mfma(lo, qs, zero);
+  for (int e = 0; e < 2; ++e) {
+    u32x4_t lo = {0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) st[i] = k_s * t[i] + k_l * la[i];
+    for (int i = 0; i < (NG + 1) / 2; ++i) lo[i] = r[e].kl[i];
+    la[e] = mfma(lo, qs, zero);
+  }
+  scale(NG - 1);
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) st[e][i] = t[e][i] * 16777216.f + la[e][i];  // the codes were c 2^-24
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 template <int D, int NG>
-__global__ void __launch_bounds__(256)
+constexpr int attend_lds() {  // the waves' tiles; then, over them, their O, m and sums
+  const int ring = 4 * 2 * 2 * Geo<D, NG>::bytes, meet = 4 * 16 * (D + 4) * 4 + 2 * 4 * 16 * 4;
+  return ring > meet ? ring : meet;
+}
+
+template <int D, int NG>
+__global__ void __launch_bounds__(256, D == 256 ? 2 : 3)
 k_qcache_attend(AttendArgs a) {
   using L = Geo<D, NG>;
   constexpr int DL = D / 16;  // dimensions of a lane of V^T p, MFMAs of it
-  __shared__ __align__(16) float s_o[4][16][D + 4];
-  __shared__ float s_m[4][16], s_l[4][16];
+  __shared__ __align__(16) uint8_t lds[attend_lds<D, NG>()];
+  float(*s_o)[16][D + 4] = (float(*)[16][D + 4])lds;
+  float(*s_m)[16] = (float(*)[16])(lds + 4 * 16 * (D + 4) * 4);
+  float(*s_l)[16] = s_m + 4;
   const int lane = threadIdx.x & 63, n = lane & 15, kq = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint8_t* ring = lds + w * (4 * L::bytes);  // two tiles
   const Seqs& sq = a.sq;
 
-  // The range [b0, b1) of this workgroup in the list of all blocks, and the sequence it starts in.
-  int total = 0, cnt = 0, inc = 0;
-  for (int s0 = 0; s0 < sq.n_seq; s0 += 64) {
-    cnt = 0;
-    if (s0 + lane < sq.n_seq) {
-      const SeqWork x = seq_work(a, s0 + lane);
-      cnt = x.nb * x.items;
-    }
+  // The lane's sequence of the 64 from sc on, and the blocks up to its end in that chunk.
+  SeqWork mine;
+  int sc, cnt, inc;
+  auto load_chunk = [&](int s0) {
+    sc = s0;
+    mine = SeqWork{0, 0, 0, 0, 0};
+    if (s0 + lane < sq.n_seq) mine = seq_work(a, s0 + lane);
+    cnt = mine.nb * mine.items;
     inc = wave_scan(cnt);
-    total += __shfl(inc, 63);
+  };
+  auto of_lane = [&](int i) {
+    auto get = [&](int v) { return __builtin_amdgcn_readlane(v, i); };
+    return SeqWork{get(mine.len), get(mine.first), get(mine.n), get(mine.nb), get(mine.items)};
+  };
+
+  // All blocks; rows of empty sequences become 0 on the way.
+  int total = 0;
+  for (int s0 = 0; s0 < sq.n_seq; s0 += 64) {
+    load_chunk(s0);
+    total += __builtin_amdgcn_readlane(inc, 63);
+    uint64_t none = __ballot(mine.items > 0 && mine.nb == 0 && (s0 + lane) % (int)gridDim.x == (int)blockIdx.x);
+    for (; none; none &= none - 1) {
+      const SeqWork x = of_lane(__builtin_ctzll(none));
+      const int per_row = a.per * a.heads * (D / 8);
+      for (int i = 0; i < x.n; ++i)
+        for (int e = threadIdx.x; e < per_row; e += 256)
+          *(u32x4_t*)(a.out + (int64_t)(x.first + i) * a.o_ts + (int64_t)(e / (D / 8)) * a.o_hs + 8 * (e % (D / 8))) =
+              (u32x4_t){0u, 0u, 0u, 0u};
+    }
   }
   const int grid = min(a.grid, total);  // no range is empty, so an item's partials are consecutive workgroups'
-  if ((int)blockIdx.x >= grid) return;
+  int* join = a.ws_join + 4 * blockIdx.x;
+  if ((int)blockIdx.x >= grid) {
+    if (threadIdx.x == 0) join[0] = -1;
+    return;
+  }
+  // This workgroup's range [b0, b1) of all blocks, the sequence it starts in, and the place there.
   const int b0 = (int)((int64_t)blockIdx.x * total / grid), b1 = (int)((int64_t)(blockIdx.x + 1) * total / grid);
-  int s = 0, at = 0;  // sequence of b0, and b0 inside it
+  int s = 0, at = 0;
   for (int s0 = 0, base = 0; s0 < sq.n_seq; s0 += 64) {
-    if (sq.n_seq > 64) {
-      cnt = 0;
-      if (s0 + lane < sq.n_seq) {
-        const SeqWork x = seq_work(a, s0 + lane);
-        cnt = x.nb * x.items;
-      }
-      inc = wave_scan(cnt);
-    }
+    if (sc != s0) load_chunk(s0);
     const uint64_t past = __ballot(base + inc > b0);
     if (past) {
       const int i = __builtin_ctzll(past);
       s = s0 + i;
-      at = b0 - (base + __shfl(inc, i) - __shfl(cnt, i));
+      at = b0 - (base + __builtin_amdgcn_readlane(inc, i) - __builtin_amdgcn_readlane(cnt, i));
       break;
     }
-    base += __shfl(inc, 63);
+    base += __builtin_amdgcn_readlane(inc, 63);
   }
-  s = __builtin_amdgcn_readfirstlane(s);
-  at = __builtin_amdgcn_readfirstlane(at);
-  SeqWork sw = seq_work(a, s);
+  SeqWork sw = of_lane(s - sc);
   int item = at / sw.nb, blk = at - item * sw.nb;
+  int start = b0 - at;  // first block of the sequence
+  bool tail = false;
 
   for (int left = b1 - b0; left > 0;) {
     if (item == sw.items) {
+      start += sw.nb * sw.items;
       item = blk = 0;
       do {
         if (++s >= sq.n_seq) return;
-        sw = seq_work(a, s);
+        const SeqWork x = seq_work(a, s);
+        auto get = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+        sw = SeqWork{get(x.len), get(x.first), get(x.n), get(x.nb), get(x.items)};
       } while (sw.nb * sw.items == 0);
     }
-    const int k0 = blk, k1 = min(sw.nb, blk + left);
-    const int rt = item / a.heads, h = item - rt * a.heads;
+    const int k0 = blk, k1 = min(sw.nb, blk + left), nt = k1 - k0;
+    const int it = item;
+    // moved on here, in front of every branch on the lane: the loop's counters stay scalar
+    left -= nt;
+    blk = 0;
+    ++item;
+    const int rt = it / a.heads, h = it - rt * a.heads;
     const int nrows = min(16, sw.n * a.per - rt * 16);
-    left -= k1 - k0;
 
-    // The column's row, query head and number of positions it may look at.
+    // Last positions that the tile's first and last row and the column's row may look at, plus 1.
     const int r = rt * 16 + n, qi = r / a.per, hg = r - qi * a.per;
     const bool real = n < nrows;
     const int lim = real ? min(max(sw.len - sw.n + qi + 1, 0), sq.cap) : 0;
     const int lim_min = min(max(sw.len - sw.n + (rt * 16) / a.per + 1, 0), sq.cap);
     const int lim_max = min(max(sw.len - sw.n + (rt * 16 + nrows - 1) / a.per + 1, 0), sq.cap);
 
-    // q: B operands, scaled by 2^e (and by 1/16 more where the code pair stays shifted).
-    u32x4_t qf[L::ND];
-    u32x4_t qs = {0u, 0u, 0u, 0u};
-    float k_s, k_l;
+    // Loads: the pages of this wave's first 32 tiles (positions 128 k + 32 w .. + 31 for k in [k0, k1); lane
+    // 2 j + e: unit e of tile j), q, and the first tile.
+    int pg = -1;
+    auto fetch_pages = [&](int j0) {
+      const int j = j0 + (lane >> 1), u = 8 * (k0 + j) + 2 * w + (lane & 1);
+      pg = j < nt && 16 * u < lim_max ? sq.page(s, u) : -1;
+    };
+    fetch_pages(0);
+    half8_t qv[L::ND];
     {
       const uint16_t* qp = a.q + (int64_t)(sw.first + qi) * a.q_ts + (int64_t)(h * a.per + hg) * a.q_hs + 8 * kq;
-      half8_t qv[L::ND];
-      float top = 0.f;
 #pragma unroll
       for (int j = 0; j < L::ND; ++j) {
         qv[j] = (half8_t){0, 0, 0, 0, 0, 0, 0, 0};
         if (real) qv[j] = *(const half8_t*)(qp + 32 * j);
+      }
+    }
+    int p0, p1;  // pages of the two units of the tile being copied
+    auto issue = [&](int j) {
+      uint8_t* to = ring + (j & 1) * (2 * L::bytes);
+      p0 = __builtin_amdgcn_readlane(pg, 2 * (j & 31));
+      p1 = __builtin_amdgcn_readlane(pg, 2 * (j & 31) + 1);
+      const int u = 8 * (k0 + j) + 2 * w;
+      if (sq.up_shift > 0 && p0 >= 0) {
+        // both units on one page, side by side; the second may lie past the last position, but not past the page
+        copy_to_lds<2 * L::bytes>(a.cache + unit_at(p0, u, h, a.heads, sq.up_shift, L::bytes), true, to, lane);
+      } else {
+        copy_to_lds<L::bytes>(a.cache + unit_at(max(p0, 0), u, h, a.heads, sq.up_shift, L::bytes), p0 >= 0, to, lane);
+        copy_to_lds<L::bytes>(a.cache + unit_at(max(p1, 0), u + 1, h, a.heads, sq.up_shift, L::bytes), p1 >= 0,
+                              to + L::bytes, lane);
+      }
+    };
+    issue(0);
+
+    // q: B operands, scaled by 2^e (and by 1/16 more where the code pair stays shifted).
+    u32x4_t qf[L::ND];
+    u32x4_t qs = {0u, 0u, 0u, 0u};
+    float k_l, raise;  // log2 units of a score; how far a score may pass m
+    {
+      float top = 0.f;
+#pragma unroll
+      for (int j = 0; j < L::ND; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf((float)qv[j][i]));
-      }
       top = column_max(top);
       const int e = top > 0.f && top <= 65504.f ? 6 - ilogbf(top) : 0;
-      k_s = ldexpf(a.scale2, 24 - e);
-      k_l = ldexpf(a.scale2, -e);
+      // never 0, and 8 / k_l finite: both meet infinities below
+      k_l = fmaxf(ldexpf(fabsf(a.scale2), -e), 1e-37f);
+      raise = 8.f / k_l;
+      const float up = a.scale2 < 0.f ? -ldexpf(1.f, e) : ldexpf(1.f, e);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         float sum = 0.f;
@@ -468,7 +646,7 @@ k_qcache_attend(AttendArgs a) {
           float x[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            x[i] = ldexpf((float)qv[j][i], e);
+            x[i] = (float)qv[j][i] * up;
             sum += x[i];
             if (i & 2) x[i] *= 0.0625f;
           }
@@ -485,142 +663,131 @@ k_qcache_attend(AttendArgs a) {
     floatx4_t o[DL];
 #pragma unroll
     for (int j = 0; j < DL; ++j) o[j] = (floatx4_t){0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, mk = 0.f, l = 0.f;  // m in units of k_l, k_l m (0 while m is -inf), sum of p
 
-    // This wave's tiles: positions 128 k + 32 w .. + 31 for k in [k0, k1).
-    const int nt = k1 - k0;
-    int pg = -1;  // lane 2 j + e: page of unit e of tile (32 jj + j)
-    auto fetch_pages = [&](int j0) {
-      const int j = j0 + (lane >> 1), u = 8 * (k0 + j) + 2 * w + (lane & 1);
-      pg = j < nt && 16 * u < lim_max ? sq.page(s, u) : -1;
-    };
-    // Pages of tile j (of the fetched 32) into p0, p1, and its loads.
-    UnitRegs<D, NG> cur[2], nxt[2];
-    auto issue = [&](int j, UnitRegs<D, NG>(&d)[2], int (&p)[2]) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        p[e] = __builtin_amdgcn_readlane(pg, 2 * (j & 31) + e);
-        const int u = 8 * (k0 + j) + 2 * w + e;
-        // a unit on no page is masked; its loads go to the first unit of the cache
-        load_unit<D, NG>(p[e] < 0 ? a.cache : a.cache + unit_at(p[e], u, h, a.heads, sq.up_shift, L::bytes), lane,
-                         d[e]);
-      }
-    };
-    int pc[2] = {-1, -1}, pn[2] = {-1, -1};
-    fetch_pages(0);
-    issue(0, cur, pc);
     for (int j = 0; j < nt; ++j) {
+      const int base = 128 * (k0 + j) + 32 * w;
+      const bool on0 = p0 >= 0, on1 = p1 >= 0;
+      const uint8_t* here = ring + (j & 1) * (2 * L::bytes);
+      KeyRegs<D, NG> kr[2];
+      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this tile has landed
+      read_keys<D, NG>(here, lane, kr[0]);
+      read_keys<D, NG>(here + L::bytes, lane, kr[1]);
       if (j + 1 < nt) {
         if (((j + 1) & 31) == 0) fetch_pages(j + 1);
-        issue(j + 1, nxt, pn);
+        issue(j + 1);  // over the tile before this one
       }
-      const int base = 128 * (k0 + j) + 32 * w;
-      if (base < lim_max && (pc[0] >= 0 || pc[1] >= 0)) {
-        float st[2][4];
+      if (base >= lim_max || !(on0 || on1)) continue;
+      const bool edge = base + 32 > lim_min || !on0 || !on1;  // some of the tile is masked for some row
+      float st[2][4];
+      tile_scores<D, NG>(kr, qf, qs, st);
+      if (edge) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) unit_scores<D, NG>(cur[e], qf, qs, k_s, k_l, st[e]);
-        const bool edge = base + 32 > lim_min || pc[0] < 0 || pc[1] < 0;
-        u32x4_t nan_seen = {0u, 0u, 0u, 0u};  // edge tiles: FP16 1 where a visible token's value group is NaN
-        if (edge) {
-          u32x4_t bad = {0u, 0u, 0u, 0u}, vis = {0u, 0u, 0u, 0u};
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int pos = base + 16 * e + 4 * kq + i, hs = 16 * (i & 1);
-              const bool sees = pos < lim && pc[e] >= 0;
-              if (!sees) st[e][i] = -INFINITY;
-              // Value statistics of tokens that no row sees may be anything: they become 0, and so do NaN
-              // groups, whose NaN is added below only to the columns that see the token.
-              const uint16_t vs = (uint16_t)(cur[e].vs[i / 2] >> hs), vl = (uint16_t)(cur[e].vs[2 + i / 2] >> hs);
-              const bool held = pos < lim_max && pc[e] >= 0;
-              const bool drop = !held || not_finite(vs) || not_finite(vl);
-              if (drop) {
-                cur[e].vs[i / 2] &= ~(0xFFFFu << hs);
-                cur[e].vs[2 + i / 2] &= ~(0xFFFFu << hs);
-              }
-              if (held && drop) bad[2 * e + i / 2] |= 0x3C00u << hs;
-              if (sees) vis[2 * e + i / 2] |= 0x3C00u << hs;
-            }
-          if (__ballot((bad[0] | bad[1] | bad[2] | bad[3]) != 0)) {
-            const floatx4_t c = mfma(bad, vis, (floatx4_t){0.f, 0.f, 0.f, 0.f});  // per (dimension run, column)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) nan_seen[i] = c[i] > 0.f;
-          }
-        }
-        float top = st[0][0];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) top = fmaxf(top, st[i / 4][i % 4]);
-        if (__ballot(top > m + 8.f)) {
-          const float mn = fmaxf(m, column_max(top));
-          const float f = mn == m ? 1.f : exp2f(m - mn);
-          m = mn;
-          l *= f;
-#pragma unroll
-          for (int j2 = 0; j2 < DL; ++j2) o[j2] *= f;
-        }
-        const float mu = m == -INFINITY ? 0.f : m;
-        u32x4_t pf;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float p[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            p[i] = exp2f(st[e][i] - mu);
-            l += p[i];
-          }
-          pf[2 * e] = pk_h(p[0], p[1]);
-          pf[2 * e + 1] = pk_h(p[2], p[3]);
-        }
-        // Values: dword [tp][c] of unit e, nibble i -> dimension 4 c + i of tokens (2 tp, 2 tp + 1).
-#pragma unroll
-        for (int c = 0; c < L::NC; ++c) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            u32x4_t av;
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int tp = 0; tp < 2; ++tp) {
-                const uint32_t wv = i < 2 ? cur[e].v[tp * L::NC + c] : cur[e].v[tp * L::NC + c] >> 8;
-                const half2_t x = as_h2((i & 1) ? (wv & 0x00F000F0u) | 0x64006400u : (wv & 0x000F000Fu) | 0x64006400u);
-                const _Float16 inv = (_Float16)((i & 1) ? 0.0625f : 1.f), off = (_Float16)((i & 1) ? -64.f : -1024.f);
-                const half2_t q = x * (half2_t){inv, inv} + (half2_t){off, off};
-                av[2 * e + tp] = as_u32(q * as_h2(cur[e].vs[tp]) + as_h2(cur[e].vs[2 + tp]));
-              }
-            o[4 * c + i] = mfma(av, pf, o[4 * c + i]);
-          }
-        }
-        if (edge)
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (nan_seen[i])
-#pragma unroll
-              for (int j2 = 0; j2 < DL; ++j2) o[j2][i] = NAN;
+            if (!((e ? on1 : on0) && base + 16 * e + 4 * kq + i < lim)) st[e][i] = -INFINITY;
       }
+      float top = st[0][0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) top = fmaxf(top, st[i / 4][i % 4]);
+      if (__ballot(top > m + raise)) {
+        const float mn = fmaxf(m, column_max(top));
+        const float f = mn == m ? 1.f : exp2_(k_l * (m - mn));
+        m = mn;
+        mk = mn == -INFINITY ? 0.f : k_l * mn;
+        l *= f;
+#pragma unroll
+        for (int j2 = 0; j2 < DL; ++j2) o[j2] *= f;
+      }
+      u32x4_t pf;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        cur[e] = nxt[e];
-        pc[e] = pn[e];
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p[i] = exp2_(k_l * st[e][i] - mk);
+          l += p[i];
+        }
+        pf[2 * e] = pk_h(p[0], p[1]);
+        pf[2 * e + 1] = pk_h(p[2], p[3]);
+      }
+      ValueRegs<D> c[2];
+      read_values<D, NG>(here, lane, c);
+      if (edge) {
+        // Value statistics of tokens that no row sees may be anything: they become 0, and so do those of NaN
+        // groups, whose NaN goes only to the columns that see the token (one MFMA of FP16 ones: per dimension
+        // run and column, how many of the NaN groups' tokens the column sees).
+        u32x4_t bad = {0u, 0u, 0u, 0u}, vis = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int pos = base + 16 * e + 4 * kq + i, hs = 16 * (i & 1);
+            const bool on = e ? on1 : on0, held = pos < lim_max && on;
+            const uint16_t vs = (uint16_t)(c[e].vs[i / 2] >> hs), vl = (uint16_t)(c[e].vs[2 + i / 2] >> hs);
+            const bool drop = !held || not_finite(vs) || not_finite(vl);
+            if (drop) {
+              c[e].vs[i / 2] &= ~(0xFFFFu << hs);
+              c[e].vs[2 + i / 2] &= ~(0xFFFFu << hs);
+            }
+            if (held && drop) bad[2 * e + i / 2] |= 0x3C00u << hs;
+            if (pos < lim && on) vis[2 * e + i / 2] |= 0x3C00u << hs;
+          }
+        if (__ballot((bad[0] | bad[1] | bad[2] | bad[3]) != 0)) {
+          const floatx4_t x = mfma(bad, vis, (floatx4_t){0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (x[i] > 0.f)
+#pragma unroll
+              for (int j2 = 0; j2 < DL; ++j2) o[j2][i] = NAN;
+        }
+      }
+      // Values: dword [tp][cc] of unit e, nibble i -> dimension 4 cc + i of tokens (2 tp, 2 tp + 1).
+#pragma unroll
+      for (int cc = 0; cc < L::NC; ++cc) {
+        uint32_t wv[4], w8[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          wv[x] = c[x / 2].v[(x & 1) * L::NC + cc];
+          w8[x] = wv[x] >> 8;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          u32x4_t av;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const half2_t y = as_h2(and_or(i < 2 ? wv[x] : w8[x], (i & 1) ? 0x00F000F0u : 0x000F000Fu, kMagic));
+            const _Float16 inv = (_Float16)((i & 1) ? 0.0625f : 1.f), off = (_Float16)((i & 1) ? -64.f : -1024.f);
+            const half2_t q = y * (half2_t){inv, inv} + (half2_t){off, off};
+            av[x] = as_u32(q * as_h2(c[x / 2].vs[x & 1]) + as_h2(c[x / 2].vs[2 + (x & 1)]));
+          }
+          o[4 * cc + i] = mfma(av, pf, o[4 * cc + i]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
 
     // The four waves meet.  o[j][i] is dimension (4 kq + i) DL + j of column n.
+    const int tid = opaque((int)threadIdx.x);
     l = column_sum(l);
+    __syncthreads();  // every wave has read its last tile
     if (real) {
-      if (kq == 0) {
-        s_m[w][n] = m;
-        s_l[w][n] = l;
+      const int c = tid & 15, k4 = (tid >> 4) & 3;
+      if (k4 == 0) {
+        s_m[w][c] = m == -INFINITY ? m : mk;
+        s_l[w][c] = l;
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < DL; j += 4)
-          *(floatx4_t*)&s_o[w][n][(4 * kq + i) * DL + j] = (floatx4_t){o[j][i], o[j + 1][i], o[j + 2][i], o[j + 3][i]};
+          *(floatx4_t*)&s_o[w][c][(4 * k4 + i) * DL + j] = (floatx4_t){o[j][i], o[j + 1][i], o[j + 2][i], o[j + 3][i]};
     }
     __syncthreads();
     const bool whole = k0 == 0 && k1 == sw.nb;
-    for (int x = threadIdx.x; x < nrows * (D / 4); x += 256) {
+    tail = k0 == 0 && k1 < sw.nb;
+    for (int x = tid; x < nrows * (D / 4); x += 256) {
       const int row = x / (D / 4), d = 4 * (x - row * (D / 4));
       const float mx = fmaxf(fmaxf(s_m[0][row], s_m[1][row]), fmaxf(s_m[2][row], s_m[3][row]));
       const float mu = mx == -INFINITY ? 0.f : mx;
@@ -628,7 +795,7 @@ k_qcache_attend(AttendArgs a) {
       floatx4_t v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const float f = exp2f(s_m[u][row] - mu);
+        const float f = exp2_(s_m[u][row] - mu);
         sum += f * s_l[u][row];
         v += f * *(const floatx4_t*)&s_o[u][row][d];
       }
@@ -646,63 +813,64 @@ k_qcache_attend(AttendArgs a) {
         }
       }
     }
+    if (tail && tid == 0) {
+      // the workgroup of block x is the largest g with g * total / grid <= x
+      const int64_t end = start + (int64_t)(it + 1) * sw.nb;
+      *(int4*)join = make_int4((int)((end * grid - 1) / total), sw.first, it, nrows);
+    }
     __syncthreads();
-    blk = 0;
-    ++item;
   }
+  if (!tail && threadIdx.x == 0) join[0] = -1;
 }
 
-// One workgroup of D threads per (item, row of its tile): adds the item's
-// partials in order and writes the row; rows of empty sequences become 0.
+// Workgroup g adds, in order, the partials of the item that attention's
+// workgroup g began and did not finish.  Thread x takes four dimensions of a
+// row and every PG-th partial.
 template <int D>
-__global__ void __launch_bounds__(D)
+__global__ void __launch_bounds__(256)
 k_qcache_join(AttendArgs a) {
-  const int lane = threadIdx.x & 63;
-  const Seqs& sq = a.sq;
-  int total = 0, s = -1, item = 0, start = 0;  // start: first block of the sequence
-  for (int s0 = 0, ibase = 0; s0 < sq.n_seq; s0 += 64) {
-    int cb = 0, ci = 0;
-    if (s0 + lane < sq.n_seq) {
-      const SeqWork x = seq_work(a, s0 + lane);
-      ci = x.items;
-      cb = x.nb * x.items;
+  __shared__ floatx4_t s_v[256];
+  __shared__ float s_s[256];
+  const int4 j = *(const int4*)(a.ws_join + 4 * blockIdx.x);
+  const int g = blockIdx.x, last = j.x, first = j.y, item = j.z, nrows = j.w;
+  if (last < 0) return;
+  const int rt = item / a.heads, h = item - rt * a.heads;
+  const int width = nrows * (D / 4), pg = width < 256 ? 256 / width : 1;
+  for (int x0 = 0; x0 < width; x0 += 256) {
+    const int grp = pg > 1 ? threadIdx.x / width : 0;
+    const int x = pg > 1 ? threadIdx.x - grp * width : x0 + threadIdx.x;
+    const bool on = grp < pg && x < width;
+    const int row = on ? x / (D / 4) : 0, d = 4 * (x - row * (D / 4));
+    auto slot = [&](int i) { return ((int64_t)i * 2 + (i == g ? 1 : 0)) * a.rows + row; };
+    float sum = 0.f;
+    floatx4_t v = {0.f, 0.f, 0.f, 0.f};
+    if (on) {
+      float mx = -INFINITY;
+      for (int i = g; i <= last; ++i) mx = fmaxf(mx, a.ws_ml[2 * slot(i)]);
+      const float mu = mx == -INFINITY ? 0.f : mx;
+      for (int i = g + grp; i <= last; i += pg) {
+        const float f = exp2_(a.ws_ml[2 * slot(i)] - mu);
+        sum += f * a.ws_ml[2 * slot(i) + 1];
+        v += f * *(const floatx4_t*)(a.ws_o + slot(i) * D + d);
+      }
     }
-    const int ib = wave_scan(cb), ii = wave_scan(ci);
-    const uint64_t past = __ballot(ibase + ii > (int)blockIdx.x);
-    if (s < 0 && past) {
-      const int i = __builtin_ctzll(past);
-      s = s0 + i;
-      item = (int)blockIdx.x - (ibase + __shfl(ii, i) - __shfl(ci, i));
-      start = total + __shfl(ib, i) - __shfl(cb, i);
+    if (pg > 1) {
+      s_v[threadIdx.x] = v;
+      s_s[threadIdx.x] = sum;
+      __syncthreads();
+      if (on && grp == 0)
+        for (int i = 1; i < pg; ++i) {
+          v += s_v[threadIdx.x + i * width];
+          sum += s_s[threadIdx.x + i * width];
+        }
     }
-    ibase += __shfl(ii, 63);
-    total += __shfl(ib, 63);
+    if (on && grp == 0) {
+      const int rr = rt * 16 + row, i = rr / a.per;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const u32x2_t y = {pk_h(v[0] * inv, v[1] * inv), pk_h(v[2] * inv, v[3] * inv)};
+      *(u32x2_t*)(a.out + (int64_t)(first + i) * a.o_ts + (int64_t)(h * a.per + rr - i * a.per) * a.o_hs + d) = y;
+    }
   }
-  if (s < 0) return;
-  const SeqWork sw = seq_work(a, s);
-  const int rt = item / a.heads, h = item - rt * a.heads, row = blockIdx.y, rr = rt * 16 + row;
-  if (rr >= sw.n * a.per) return;
-  const int i = rr / a.per, d = threadIdx.x;
-  uint16_t* y = a.out + (int64_t)(sw.first + i) * a.o_ts + (int64_t)(h * a.per + rr - i * a.per) * a.o_hs + d;
-  if (sw.nb == 0) {
-    *y = 0;
-    return;
-  }
-  const int64_t x0 = start + (int64_t)item * sw.nb;
-  const int grid = min(a.grid, total);
-  const int ga = (int)(((x0 + 1) * grid - 1) / total), gb = (int)(((x0 + sw.nb) * grid - 1) / total);
-  if (ga == gb) return;
-  auto slot = [&](int g) { return ((int64_t)g * 2 + (g == ga ? 1 : 0)) * a.rows + row; };
-  float mx = -INFINITY;
-  for (int g = ga; g <= gb; ++g) mx = fmaxf(mx, a.ws_ml[2 * slot(g)]);
-  const float mu = mx == -INFINITY ? 0.f : mx;
-  float sum = 0.f, v = 0.f;
-  for (int g = ga; g <= gb; ++g) {
-    const float f = exp2f(a.ws_ml[2 * slot(g)] - mu);
-    sum += f * a.ws_ml[2 * slot(g) + 1];
-    v += f * a.ws_o[slot(g) * D + d];
-  }
-  *y = f2h(sum == 0.f ? 0.f : v / sum);
 }
 
 // ---- host side ----------------------------------------------------------------
@@ -789,11 +957,9 @@ hipError_t launch_read(Dims<D, NG>, const uint8_t* cache, const Seqs& sq, const 
   return hipGetLastError();
 }
 
-// The launch of an attention call: workgroups, partial rows per slot, and an
-// upper bound of the items (row tiles times heads) for the join.
+// The launch of an attention call: workgroups, and partial rows per slot.
 struct AttendPlan {
   int grid, rows;
-  int64_t items;
   size_t bytes;
 };
 
@@ -807,15 +973,19 @@ int attend_plan(const qcache_shape* sh, const qcache_seqs* sq, int32_t n_q_heads
   // a sequence of n rows has ceil(n per / 16) tiles: at most n per / 16 + 1, and one per sequence with one row each
   const int64_t tiles = sq->q_start ? sq->n_seq + (int64_t)sq->n_tok * per / 16
                                     : (int64_t)sq->n_seq * ((per + 15) / 16);
-  p.items = tiles * sh->n_heads;
+  const int64_t items = tiles * sh->n_heads;
   const int64_t cap = (int64_t)sq->max_pages * sh->page_size;
   const int64_t blocks = (cap + kBlock - 1) / kBlock;
-  if (p.items > 0x7FFFFFFF || (blocks > 0 && p.items > 0x7FFFFFFF / blocks)) return QGEMV_ERR_UNSUPPORTED;
+  if (items > 0x7FFFFFFF || (blocks > 0 && items > 0x7FFFFFFF / blocks)) return QGEMV_ERR_UNSUPPORTED;
   if ((int64_t)sq->n_tok * per > 0x7FFFFFFF - 16) return QGEMV_ERR_UNSUPPORTED;
-  const int64_t all = p.items * blocks;
-  p.grid = all < 1 ? 1 : all < 1024 ? (int)all : 1024;
+  const int64_t all = items * blocks;
+  // As many workgroups as the 256 CUs hold at once (their registers allow 4, 3 and 2 a CU): with more, the last
+  // ones start when the first have ended and the launch takes two rounds (attend_one_long, 32 heads x 32768
+  // positions: 51 us with 1024 workgroups of head_dim 128).
+  const int most = 256 * (sh->head_dim == 64 ? 4 : sh->head_dim == 128 ? 3 : 2);
+  p.grid = all < 1 ? 1 : all < most ? (int)all : most;
   p.rows = sq->q_start || per > 16 ? 16 : per;
-  p.bytes = (size_t)p.grid * 2 * p.rows * (sh->head_dim + 2) * 4;
+  p.bytes = (size_t)p.grid * (2 * (size_t)p.rows * (sh->head_dim + 2) * 4 + 16);
   return QGEMV_OK;
 }
 
@@ -824,7 +994,7 @@ hipError_t launch_attend(Dims<D, NG>, const AttendArgs& a, const AttendPlan& p, 
   hipLaunchKernelGGL((k_qcache_attend<D, NG>), dim3(p.grid), dim3(256), 0, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_qcache_join<D>), dim3((uint32_t)p.items, p.rows), dim3(D), 0, st, a);
+  hipLaunchKernelGGL((k_qcache_join<D>), dim3(p.grid), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
@@ -904,6 +1074,7 @@ int qcache_attend(const qcache_shape* shape, const void* cache, const qcache_seq
   a.o_hs = out->head_stride;
   a.ws_o = (float*)ws;
   a.ws_ml = a.ws_o + (size_t)p.grid * 2 * p.rows * shape->head_dim;
+  a.ws_join = (int*)(a.ws_ml + (size_t)p.grid * 2 * p.rows * 2);
   a.heads = shape->n_heads;
   a.per = n_q_heads / shape->n_heads;
   a.rows = p.rows;
