@@ -269,6 +269,30 @@ k_qcache_read(const uint8_t* __restrict__ cache, Seqs sq, Rows k, Rows v, int he
 // workgroup leaves a partial (at most two per workgroup: the item it starts in,
 // slot 0, and the one it ends in, slot 1), and k_qcache_join adds them in order.
 // ---------------------------------------------------------------------------
+// x / d for 0 <= x < 2^31 as a multiplication: M = 2^(31 + sh) / d + 1, 2^(sh - 1) < d <= 2^sh.
+struct Divisor {
+  uint32_t d, mul, sh;
+  __device__ __forceinline__ int of(int x) const {
+    return d == 1 ? x : (int)(__umulhi((uint32_t)x, mul) >> (sh - 1));
+  }
+};
+inline Divisor divisor(int d) {
+  uint32_t sh = 0;
+  while ((1u << sh) < (uint32_t)d) ++sh;
+  return Divisor{(uint32_t)d, (uint32_t)((((uint64_t)1 << (31 + sh)) / (uint32_t)d) + 1), sh};
+}
+
+// How `total` blocks are cut into `grid` ranges: the first rem have q + 1, the others q.
+struct Cut {
+  int q, rem;
+  __device__ __forceinline__ Cut(int total, int grid) : q(total / grid), rem(total - total / grid * grid) {}
+  __device__ __forceinline__ int begin(int g) const { return g * q + min(g, rem); }
+  __device__ __forceinline__ int range_of(int x) const {  // the range of block x
+    const int y = x - rem * (q + 1);
+    return y < 0 ? x / (q + 1) : rem + y / q;
+  }
+};
+
 struct AttendArgs {
   Seqs sq;
   const uint8_t* cache;
@@ -279,12 +303,17 @@ struct AttendArgs {
   float* ws_ml;  // [grid][2][rows][2]: m (log2), sum
   int* ws_join;  // [grid][4]: last workgroup of the item that this one ends in (-1: none), its first row, item, rows
   int heads, per, rows, grid;
+  int whole;  // ranges are cut between items only: every item is one workgroup's
+  Divisor by_heads, by_per;
   float scale2;  // scale * log2 e
 };
 
-// Blocks per item and items of sequence s.
+// Sequence s: its length, first row and rows, the blocks of an item, an item's cost and the items.  The cost is what
+// ranges are cut by: one per block and kItemCost for the item's start and end (its pages and q, the waves'
+// meeting), which come after the blocks; or 1, where ranges are cut between items only.
+constexpr int kItemCost = 3;
 struct SeqWork {
-  int len, first, n, nb, items;
+  int len, first, n, nb, cost, items;
 };
 __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int s) {
   SeqWork w;
@@ -292,7 +321,8 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int s) {
   w.n = a.sq.q_start ? max(a.sq.start(s + 1) - w.first, 0) : 1;
   w.len = a.sq.lens[s];  // not cut to cap: positions count from the true end
   w.nb = (min(max(w.len, 0), a.sq.cap) + kBlock - 1) / kBlock;
-  w.items = (int)(((int64_t)w.n * a.per + 15) / 16) * a.heads;
+  w.cost = w.nb == 0 ? 0 : a.whole ? 1 : w.nb + kItemCost;
+  w.items = ((w.n * a.per + 15) >> 4) * a.heads;
   return w;
 }
 
@@ -309,13 +339,19 @@ __device__ __forceinline__ int wave_scan(int v) {  // inclusive
   return dpp_add<0x143, 0xC>(v);  // lane 31 to rows 2, 3
 }
 
-__device__ __forceinline__ float column_max(float v) {  // over the four lanes of a column
-  v = fmaxf(v, __shfl_xor(v, 16));
-  return fmaxf(v, __shfl_xor(v, 32));
+// Lanes i ^ 16, then i ^ 32: each swap leaves the two partners' values in x and y.
+template <class Op>
+__device__ __forceinline__ float over_column(float v, Op op) {  // the four lanes of a column
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = op(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return op(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float column_max(float v) {
+  return over_column(v, [](float x, float y) { return fmaxf(x, y); });
 }
 __device__ __forceinline__ float column_sum(float v) {
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
+  return over_column(v, [](float x, float y) { return x + y; });
 }
 
 typedef float floatx2_t __attribute__((ext_vector_type(2)));
@@ -486,6 +522,9 @@ __device__ __forceinline__ void tile_scores(const KeyRegs<D, NG> (&r)[2], const 
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// Workgroups of a CU at once, by their registers.
+constexpr int attend_resident(int D) { return D == 256 ? 2 : D == 128 ? 3 : 4; }
+
 template <int D, int NG>
 constexpr int attend_lds() {  // the waves' tiles; then, over them, their O, m and sums
   const int ring = 4 * 2 * 2 * Geo<D, NG>::bytes, meet = 4 * 16 * (D + 4) * 4 + 2 * 4 * 16 * 4;
@@ -493,7 +532,7 @@ constexpr int attend_lds() {  // the waves' tiles; then, over them, their O, m a
 }
 
 template <int D, int NG>
-__global__ void __launch_bounds__(256, D == 256 ? 2 : 3)
+__global__ void __launch_bounds__(256, attend_resident(D))
 k_qcache_attend(AttendArgs a) {
   using L = Geo<D, NG>;
   constexpr int DL = D / 16;  // dimensions of a lane of V^T p, MFMAs of it
@@ -511,14 +550,14 @@ k_qcache_attend(AttendArgs a) {
   int sc, cnt, inc;
   auto load_chunk = [&](int s0) {
     sc = s0;
-    mine = SeqWork{0, 0, 0, 0, 0};
+    mine = SeqWork{0, 0, 0, 0, 0, 0};
     if (s0 + lane < sq.n_seq) mine = seq_work(a, s0 + lane);
-    cnt = mine.nb * mine.items;
+    cnt = mine.cost * mine.items;
     inc = wave_scan(cnt);
   };
   auto of_lane = [&](int i) {
     auto get = [&](int v) { return __builtin_amdgcn_readlane(v, i); };
-    return SeqWork{get(mine.len), get(mine.first), get(mine.n), get(mine.nb), get(mine.items)};
+    return SeqWork{get(mine.len), get(mine.first), get(mine.n), get(mine.nb), get(mine.cost), get(mine.items)};
   };
 
   // All blocks; rows of empty sequences become 0 on the way.
@@ -526,7 +565,8 @@ k_qcache_attend(AttendArgs a) {
   for (int s0 = 0; s0 < sq.n_seq; s0 += 64) {
     load_chunk(s0);
     total += __builtin_amdgcn_readlane(inc, 63);
-    uint64_t none = __ballot(mine.items > 0 && mine.nb == 0 && (s0 + lane) % (int)gridDim.x == (int)blockIdx.x);
+    uint64_t none = __ballot(mine.items > 0 && mine.nb == 0);
+    if (none) none = __ballot(mine.items > 0 && mine.nb == 0 && (s0 + lane) % (int)gridDim.x == (int)blockIdx.x);
     for (; none; none &= none - 1) {
       const SeqWork x = of_lane(__builtin_ctzll(none));
       const int per_row = a.per * a.heads * (D / 8);
@@ -543,7 +583,8 @@ k_qcache_attend(AttendArgs a) {
     return;
   }
   // This workgroup's range [b0, b1) of all blocks, the sequence it starts in, and the place there.
-  const int b0 = (int)((int64_t)blockIdx.x * total / grid), b1 = (int)((int64_t)(blockIdx.x + 1) * total / grid);
+  const Cut cut(total, grid);
+  const int b0 = cut.begin(blockIdx.x), b1 = cut.begin(blockIdx.x + 1);
   int s = 0, at = 0;
   for (int s0 = 0, base = 0; s0 < sq.n_seq; s0 += 64) {
     if (sc != s0) load_chunk(s0);
@@ -557,36 +598,38 @@ k_qcache_attend(AttendArgs a) {
     base += __builtin_amdgcn_readlane(inc, 63);
   }
   SeqWork sw = of_lane(s - sc);
-  int item = at / sw.nb, blk = at - item * sw.nb;
-  int start = b0 - at;  // first block of the sequence
+  int item = at / sw.cost, blk = at - item * sw.cost;
+  int start = b0 - at;  // first part of the sequence
   bool tail = false;
 
   for (int left = b1 - b0; left > 0;) {
     if (item == sw.items) {
-      start += sw.nb * sw.items;
+      start += sw.cost * sw.items;
       item = blk = 0;
       do {
         if (++s >= sq.n_seq) return;
         const SeqWork x = seq_work(a, s);
         auto get = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
-        sw = SeqWork{get(x.len), get(x.first), get(x.n), get(x.nb), get(x.items)};
-      } while (sw.nb * sw.items == 0);
+        sw = SeqWork{get(x.len), get(x.first), get(x.n), get(x.nb), get(x.cost), get(x.items)};
+      } while (sw.cost * sw.items == 0);
     }
-    const int k0 = blk, k1 = min(sw.nb, blk + left), nt = k1 - k0;
+    const int parts = min(sw.cost - blk, left);
+    const int k0 = blk, k1 = a.whole ? sw.nb : min(blk + parts, sw.nb), nt = k1 - k0;
     const int it = item;
     // moved on here, in front of every branch on the lane: the loop's counters stay scalar
-    left -= nt;
+    left -= parts;
     blk = 0;
     ++item;
-    const int rt = it / a.heads, h = it - rt * a.heads;
+    if (nt <= 0) continue;  // only the cost of its end
+    const int rt = a.by_heads.of(it), h = it - rt * a.heads;
     const int nrows = min(16, sw.n * a.per - rt * 16);
 
     // Last positions that the tile's first and last row and the column's row may look at, plus 1.
-    const int r = rt * 16 + n, qi = r / a.per, hg = r - qi * a.per;
+    const int r = rt * 16 + n, qi = a.by_per.of(r), hg = r - qi * a.per;
     const bool real = n < nrows;
     const int lim = real ? min(max(sw.len - sw.n + qi + 1, 0), sq.cap) : 0;
-    const int lim_min = min(max(sw.len - sw.n + (rt * 16) / a.per + 1, 0), sq.cap);
-    const int lim_max = min(max(sw.len - sw.n + (rt * 16 + nrows - 1) / a.per + 1, 0), sq.cap);
+    const int lim_min = min(max(sw.len - sw.n + a.by_per.of(rt * 16) + 1, 0), sq.cap);
+    const int lim_max = min(max(sw.len - sw.n + a.by_per.of(rt * 16 + nrows - 1) + 1, 0), sq.cap);
 
     // Loads: the pages of this wave's first 32 tiles (positions 128 k + 32 w .. + 31 for k in [k0, k1); lane
     // 2 j + e: unit e of tile j), q, and the first tile.
@@ -800,7 +843,7 @@ k_qcache_attend(AttendArgs a) {
         v += f * *(const floatx4_t*)&s_o[u][row][d];
       }
       if (whole) {
-        const int rr = rt * 16 + row, i = rr / a.per;
+        const int rr = rt * 16 + row, i = a.by_per.of(rr);
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const u32x2_t y = {pk_h(v[0] * inv, v[1] * inv), pk_h(v[2] * inv, v[3] * inv)};
         *(u32x2_t*)(a.out + (int64_t)(sw.first + i) * a.o_ts + (int64_t)(h * a.per + rr - i * a.per) * a.o_hs + d) = y;
@@ -814,9 +857,7 @@ k_qcache_attend(AttendArgs a) {
       }
     }
     if (tail && tid == 0) {
-      // the workgroup of block x is the largest g with g * total / grid <= x
-      const int64_t end = start + (int64_t)(it + 1) * sw.nb;
-      *(int4*)join = make_int4((int)((end * grid - 1) / total), sw.first, it, nrows);
+      *(int4*)join = make_int4(cut.range_of(start + it * sw.cost + sw.nb - 1), sw.first, it, nrows);
     }
     __syncthreads();
   }
@@ -825,48 +866,51 @@ k_qcache_attend(AttendArgs a) {
 
 // Workgroup g adds, in order, the partials of the item that attention's
 // workgroup g began and did not finish.  Thread x takes four dimensions of a
-// row and every PG-th partial.
+// row and every PG-th partial, then PG threads' sums meet in LDS.
+constexpr int kJoinThreads = 512;
 template <int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kJoinThreads)
 k_qcache_join(AttendArgs a) {
-  __shared__ floatx4_t s_v[256];
-  __shared__ float s_s[256];
+  __shared__ floatx4_t s_v[kJoinThreads];
+  __shared__ float s_m[kJoinThreads], s_l[kJoinThreads];
   const int4 j = *(const int4*)(a.ws_join + 4 * blockIdx.x);
   const int g = blockIdx.x, last = j.x, first = j.y, item = j.z, nrows = j.w;
   if (last < 0) return;
-  const int rt = item / a.heads, h = item - rt * a.heads;
-  const int width = nrows * (D / 4), pg = width < 256 ? 256 / width : 1;
-  for (int x0 = 0; x0 < width; x0 += 256) {
-    const int grp = pg > 1 ? threadIdx.x / width : 0;
-    const int x = pg > 1 ? threadIdx.x - grp * width : x0 + threadIdx.x;
-    const bool on = grp < pg && x < width;
-    const int row = on ? x / (D / 4) : 0, d = 4 * (x - row * (D / 4));
-    auto slot = [&](int i) { return ((int64_t)i * 2 + (i == g ? 1 : 0)) * a.rows + row; };
-    float sum = 0.f;
+  const int rt = a.by_heads.of(item), h = item - rt * a.heads;
+  static_assert(16 * (256 / 4) <= 2 * kJoinThreads, "at most two passes");
+  const int width = min(nrows * (D / 4), kJoinThreads), pg = kJoinThreads / width;
+  const int grp = threadIdx.x / width, x1 = threadIdx.x - grp * width;
+  for (int x0 = 0; x0 < nrows * (D / 4); x0 += width) {
+    const int x = x0 + x1, row = x / (D / 4), d = 4 * (x - row * (D / 4));
+    const bool on = grp < pg && row < nrows;
+    float m = -INFINITY, l = 0.f;
     floatx4_t v = {0.f, 0.f, 0.f, 0.f};
+    auto add = [&](float pm, float pl, floatx4_t pv) {
+      const float mn = fmaxf(m, pm), mu = mn == -INFINITY ? 0.f : mn;
+      const float f = exp2_(m - mu), pf = exp2_(pm - mu);
+      l = f * l + pf * pl;
+      v = f * v + pf * pv;
+      m = mn;
+    };
     if (on) {
-      float mx = -INFINITY;
-      for (int i = g; i <= last; ++i) mx = fmaxf(mx, a.ws_ml[2 * slot(i)]);
-      const float mu = mx == -INFINITY ? 0.f : mx;
+#pragma unroll 4
       for (int i = g + grp; i <= last; i += pg) {
-        const float f = exp2_(a.ws_ml[2 * slot(i)] - mu);
-        sum += f * a.ws_ml[2 * slot(i) + 1];
-        v += f * *(const floatx4_t*)(a.ws_o + slot(i) * D + d);
+        const int64_t slot = ((int64_t)i * 2 + (i == g ? 1 : 0)) * a.rows + row;
+        const floatx2_t ml = *(const floatx2_t*)(a.ws_ml + 2 * slot);
+        add(ml[0], ml[1], *(const floatx4_t*)(a.ws_o + slot * D + d));
       }
     }
     if (pg > 1) {
       s_v[threadIdx.x] = v;
-      s_s[threadIdx.x] = sum;
+      s_m[threadIdx.x] = m;
+      s_l[threadIdx.x] = l;
       __syncthreads();
       if (on && grp == 0)
-        for (int i = 1; i < pg; ++i) {
-          v += s_v[threadIdx.x + i * width];
-          sum += s_s[threadIdx.x + i * width];
-        }
+        for (int i = 1; i < pg; ++i) add(s_m[x1 + i * width], s_l[x1 + i * width], s_v[x1 + i * width]);
     }
     if (on && grp == 0) {
-      const int rr = rt * 16 + row, i = rr / a.per;
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const int rr = rt * 16 + row, i = a.by_per.of(rr);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
       const u32x2_t y = {pk_h(v[0] * inv, v[1] * inv), pk_h(v[2] * inv, v[3] * inv)};
       *(u32x2_t*)(a.out + (int64_t)(first + i) * a.o_ts + (int64_t)(h * a.per + rr - i * a.per) * a.o_hs + d) = y;
     }
@@ -960,6 +1004,7 @@ hipError_t launch_read(Dims<D, NG>, const uint8_t* cache, const Seqs& sq, const 
 // The launch of an attention call: workgroups, and partial rows per slot.
 struct AttendPlan {
   int grid, rows;
+  bool whole;
   size_t bytes;
 };
 
@@ -976,13 +1021,15 @@ int attend_plan(const qcache_shape* sh, const qcache_seqs* sq, int32_t n_q_heads
   const int64_t items = tiles * sh->n_heads;
   const int64_t cap = (int64_t)sq->max_pages * sh->page_size;
   const int64_t blocks = (cap + kBlock - 1) / kBlock;
-  if (items > 0x7FFFFFFF || (blocks > 0 && items > 0x7FFFFFFF / blocks)) return QGEMV_ERR_UNSUPPORTED;
+  if (items > 0x7FFFFFFF / (blocks + kItemCost)) return QGEMV_ERR_UNSUPPORTED;
   if ((int64_t)sq->n_tok * per > 0x7FFFFFFF - 16) return QGEMV_ERR_UNSUPPORTED;
-  const int64_t all = items * blocks;
-  // As many workgroups as the 256 CUs hold at once (their registers allow 4, 3 and 2 a CU): with more, the last
-  // ones start when the first have ended and the launch takes two rounds (attend_one_long, 32 heads x 32768
-  // positions: 51 us with 1024 workgroups of head_dim 128).
-  const int most = 256 * (sh->head_dim == 64 ? 4 : sh->head_dim == 128 ? 3 : 2);
+  // Up to 4 blocks an item (by the table's width, which the host knows): a workgroup takes whole items, and there
+  // is nothing to join.  A further block costs it about 1.5 us, the join's launch 5 us.
+  p.whole = blocks <= 4;
+  // As many workgroups as the 256 CUs hold at once: with more, the last ones start when the first have ended and
+  // the launch takes two rounds (32 heads x 32768 positions: 51 us with 1024 workgroups where 768 fit, 40 with 768).
+  const int64_t all = p.whole ? items : items * blocks;
+  const int most = 256 * attend_resident(sh->head_dim);
   p.grid = all < 1 ? 1 : all < most ? (int)all : most;
   p.rows = sq->q_start || per > 16 ? 16 : per;
   p.bytes = (size_t)p.grid * (2 * (size_t)p.rows * (sh->head_dim + 2) * 4 + 16);
@@ -993,8 +1040,8 @@ template <int D, int NG>
 hipError_t launch_attend(Dims<D, NG>, const AttendArgs& a, const AttendPlan& p, hipStream_t st) {
   hipLaunchKernelGGL((k_qcache_attend<D, NG>), dim3(p.grid), dim3(256), 0, st, a);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_qcache_join<D>), dim3(p.grid), dim3(256), 0, st, a);
+  if (e != hipSuccess || p.whole) return e;
+  hipLaunchKernelGGL((k_qcache_join<D>), dim3(p.grid), dim3(kJoinThreads), 0, st, a);
   return hipGetLastError();
 }
 
@@ -1079,6 +1126,9 @@ int qcache_attend(const qcache_shape* shape, const void* cache, const qcache_seq
   a.per = n_q_heads / shape->n_heads;
   a.rows = p.rows;
   a.grid = p.grid;
+  a.whole = p.whole;
+  a.by_heads = divisor(a.heads);
+  a.by_per = divisor(a.per);
   a.scale2 = scale * 1.4426950408889634f;
   return hip_status(by_shape(shape, [&](auto d) { return launch_attend(d, a, p, (hipStream_t)stream); }));
 }
