@@ -42,24 +42,6 @@ struct Seqs {
   __device__ __forceinline__ int start(int s) const {
     return q_start ? min(max(q_start[s], 0), n_tok) : s;
   }
-  // Sequence of row t (-1: padding) and the row's position in it (may be negative).
-  __device__ __forceinline__ int find(int t, int& pos) const {
-    int s = t, first = t, n = 1;
-    if (q_start) {
-      int lo = 0, hi = n_seq;  // the last s with start(s) <= t
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (start(mid) <= t) lo = mid;
-        else hi = mid;
-      }
-      s = lo;
-      first = start(s);
-      n = start(s + 1) - first;
-      if (t < first || t >= first + n) return -1;
-    }
-    pos = max(lens[s], 0) - n + (t - first);
-    return s;
-  }
   // Page of unit u (of 16 positions) of sequence s, or -1.
   __device__ __forceinline__ int page(int s, int u) const {
     const int i = u >> up_shift;
@@ -80,159 +62,444 @@ struct Rows {
   int f32;
 };
 
-__device__ __forceinline__ void load8(const Rows& r, int64_t e, float (&v)[8]) {
+// A register that another lane is about to read (a lane swap, DPP) has to have been written two instructions before.
+// The compiler sees to that after its own instructions, but it does not look into inline asm (pk_min below).
+__device__ __forceinline__ uint32_t settled(uint32_t v) {
+  asm("s_nop 1" : "+v"(v));
+  return v;
+}
+
+// Lanes i ^ 16, then i ^ 32: each swap leaves the two partners' values in its two results.
+template <class Op>
+__device__ __forceinline__ uint32_t over_column(uint32_t v, Op op) {  // the four lanes of a column
+  v = settled(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = settled(op(a[0], a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return op(b[0], b[1]);
+}
+__device__ __forceinline__ float column_max(float v) {
+  return __uint_as_float(over_column(__float_as_uint(v), [](uint32_t x, uint32_t y) {
+    return __float_as_uint(fmaxf(__uint_as_float(x), __uint_as_float(y)));
+  }));
+}
+__device__ __forceinline__ float column_sum(float v) {
+  return __uint_as_float(over_column(__float_as_uint(v), [](uint32_t x, uint32_t y) {
+    return __float_as_uint(__uint_as_float(x) + __uint_as_float(y));
+  }));
+}
+
+typedef float floatx2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pk_h(float a, float b) {  // round to nearest even
+  return as_u32(__builtin_convertvector((floatx2_t){a, b}, half2_t));
+}
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }  // 1 ulp; results below 2^-126 are 0
+
+
+// x / d for 0 <= x < 2^31 as a multiplication: M = 2^(31 + sh) / d + 1, 2^(sh - 1) < d <= 2^sh.
+struct Divisor {
+  uint32_t d, mul, sh;
+  __device__ __forceinline__ int of(int x) const {
+    return d == 1 ? x : (int)(__umulhi((uint32_t)x, mul) >> (sh - 1));
+  }
+};
+inline Divisor divisor(int d) {
+  uint32_t sh = 0;
+  while ((1u << sh) < (uint32_t)d) ++sh;
+  return Divisor{(uint32_t)d, (uint32_t)((((uint64_t)1 << (31 + sh)) / (uint32_t)d) + 1), sh};
+}
+
+// ---------------------------------------------------------------------------
+// Writing and reading back.
+//
+// A wave takes the keys, or the values, of one unit (16 positions of one
+// head), and a lane holds of them what it holds in the attention's operands:
+// of the keys one token and D/32 runs of 8 dimensions, of the values D/16
+// dimensions of four tokens.  So a unit's codes are one contiguous 16 bytes
+// a lane (head_dim 128), and rows of FP16 or fp32 are read and written in runs
+// of 16 bytes or more.  Both kernels are bound by HBM.
+//
+// Waves are numbered without knowing the lengths: sequence s owns the numbers
+// from (its first row / 16) + 2 s on, which leaves room for a unit at either end
+// that its rows only partly fill.
+// ---------------------------------------------------------------------------
+struct UnitTask {
+  int s, u;        // sequence (-1: none) and unit (may be negative)
+  int row, n, p0;  // rows [row, row + n) stand at positions p0 ..
+};
+__device__ __forceinline__ UnitTask unit_task(const Seqs& sq, int idx) {
+  UnitTask x;
+  x.s = -1;
+  if (!sq.q_start) {
+    if (idx >= sq.n_seq) return x;
+    x.s = x.row = idx;
+    x.n = 1;
+    x.p0 = max(sq.lens[idx], 0) - 1;
+    x.u = x.p0 >> 4;
+    return x;
+  }
+  // the last s whose first number is at most idx, 64 probes at a time
+  auto number = [&](int s) { return (sq.start(s) >> 4) + 2 * s; };
+  const int lane = threadIdx.x & 63;
+  int lo = 0;
+  for (int cnt = sq.n_seq; cnt > 1;) {
+    const int step = (cnt + 63) >> 6, s = lo + lane * step;
+    const int c = __builtin_popcountll(__ballot(s < lo + cnt && number(s) <= idx));
+    const int skip = max(c - 1, 0) * step;
+    lo += skip;
+    cnt = min(step, cnt - skip);
+  }
+  x.row = sq.start(lo);
+  x.n = sq.start(lo + 1) - x.row;
+  if (x.n <= 0) return x;
+  x.p0 = max(sq.lens[lo], 0) - x.n;
+  x.u = (x.p0 >> 4) + idx - number(lo);
+  if (16 * x.u >= x.p0 + x.n) return x;
+  x.s = lo;
+  return x;
+}
+inline int unit_waves(const Seqs& sq) { return sq.q_start ? sq.n_tok / 16 + 2 * sq.n_seq : sq.n_seq; }
+
+// N consecutive elements (a multiple of 4) as FP16 pairs / from fp32.
+template <int N>
+__device__ __forceinline__ void load_pairs(const Rows& r, int64_t e, uint32_t* h) {
   if (r.f32) {
-    const floatx4_t a = ((const floatx4_t*)((const float*)r.data + e))[0], b = ((const floatx4_t*)((const float*)r.data + e))[1];
+    const floatx4_t* p = (const floatx4_t*)((const float*)r.data + e);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = a[i];
-      v[4 + i] = b[i];
+    for (int i = 0; i < N / 4; ++i) {
+      const floatx4_t x = p[i];
+      h[2 * i] = pk_h(x[0], x[1]);
+      h[2 * i + 1] = pk_h(x[2], x[3]);
+    }
+  } else if constexpr (N % 8 == 0) {
+    const u32x4_t* p = (const u32x4_t*)((const _Float16*)r.data + e);
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) {
+      const u32x4_t x = p[i];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) h[4 * i + k] = x[k];
     }
   } else {
-    const half8_t a = *(const half8_t*)((const _Float16*)r.data + e);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (float)a[i];
+    const u32x2_t x = *(const u32x2_t*)((const _Float16*)r.data + e);
+    h[0] = x[0], h[1] = x[1];
   }
 }
-__device__ __forceinline__ void store8(const Rows& r, int64_t e, const float (&v)[8]) {
+template <int N>
+__device__ __forceinline__ void store_values(const Rows& r, int64_t e, const float* v) {
   if (r.f32) {
     floatx4_t* p = (floatx4_t*)((float*)r.data + e);
-    p[0] = (floatx4_t){v[0], v[1], v[2], v[3]};
-    p[1] = (floatx4_t){v[4], v[5], v[6], v[7]};
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) p[i] = (floatx4_t){v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+  } else if constexpr (N % 8 == 0) {
+    u32x4_t* p = (u32x4_t*)((_Float16*)r.data + e);
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) {
+      u32x4_t x;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = pk_h(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
+      p[i] = x;
+    }
   } else {
-    half8_t a;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = (_Float16)v[i];
-    *(half8_t*)((_Float16*)r.data + e) = a;
+    *(u32x2_t*)((_Float16*)r.data + e) = (u32x2_t){pk_h(v[0], v[1]), pk_h(v[2], v[3])};
   }
 }
 
-// ---------------------------------------------------------------------------
-// Quantising.  A thread takes 8 consecutive dimensions of one token and head:
-// D/8 neighbouring lanes a vector, G/8 (4, 8 or 16, inside one DPP row) a group.
-// ---------------------------------------------------------------------------
+// Minimum and maximum of FP16 pairs, written out: the compiler's own quieten their operands first, which doubles them.
+__device__ __forceinline__ uint32_t pk_min(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("v_pk_min_f16 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("v_pk_max_f16 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
+  return d;
+}
+// (min of the low halves, min of the negated high halves)
+__device__ __forceinline__ uint32_t pk_min_neg(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("v_pk_min_f16 %0, %1, %2 neg_hi:[1,1]" : "=v"(d) : "v"(a), "v"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pk_max_u16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("v_pk_max_u16 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
+  return d;
+}
+
+// Of FP16 pairs: (smallest, -largest), and the largest |bits| of either half.  0x7C00 and more are not finite; the
+// minimum passes a NaN by.
+struct Extent {
+  uint32_t ends, top;
+};
 template <int N>
-__device__ __forceinline__ void group_min_max(float& lo, float& hi) {
-  lo = fminf(lo, dpp_mov<0xB1, 0xF>(lo)), hi = fmaxf(hi, dpp_mov<0xB1, 0xF>(hi));  // lanes i ^ 1
-  lo = fminf(lo, dpp_mov<0x4E, 0xF>(lo)), hi = fmaxf(hi, dpp_mov<0x4E, 0xF>(hi));  // i ^ 2
-  if constexpr (N > 4)  // the other four of eight
-    lo = fminf(lo, dpp_mov<0x141, 0xF>(lo)), hi = fmaxf(hi, dpp_mov<0x141, 0xF>(hi));
-  if constexpr (N > 8)  // the other eight of sixteen
-    lo = fminf(lo, dpp_mov<0x140, 0xF>(lo)), hi = fmaxf(hi, dpp_mov<0x140, 0xF>(hi));
+__device__ __forceinline__ Extent extent(const uint32_t* h) {
+  uint32_t lo = h[0], hi = h[0], top = h[0] & 0x7FFF7FFFu;
+#pragma unroll
+  for (int i = 1; i < N; ++i) {
+    lo = pk_min(lo, h[i]);
+    hi = pk_max(hi, h[i]);
+    top = pk_max_u16(top, h[i] & 0x7FFF7FFFu);
+  }
+  return Extent{pk_min_neg(perm(hi, lo, 0x05040100u), perm(hi, lo, 0x07060302u)), top};
+}
+__device__ __forceinline__ bool bad_top(uint32_t t) { return (t & 0xFFFFu) >= 0x7C00u || t >= 0x7C000000u; }
+
+// What a group's codes are formed with.  A quotient a / b is formed as q0 = a y, q0 + (a - q0 b) y, with y = 1 / b to
+// about an ulp: a - q0 b is exact, so the sum is within 2^-45 of a / b before its one rounding, and a / b, a of 24 bits
+// over b of 11 (s) or 4 (15), is no nearer than 2^-36 to a rounding border without lying on it: it is fp32(a / b).
+struct Step {
+  float lo, s, inv;
+  uint16_t s16, lo16;
+};
+__device__ __forceinline__ float quotient(float a, float b, float y) {
+  const float q0 = a * y;
+  return __builtin_fmaf(__builtin_fmaf(-q0, b, a), y, q0);
+}
+__device__ __forceinline__ Step make_step(uint32_t ends, bool bad) {
+  Step t;
+  t.lo16 = (uint16_t)ends;
+  t.lo = h2f(t.lo16);
+  uint16_t s = f2h(quotient(-h2f((uint16_t)(ends >> 16)) - t.lo, 15.f, 1.f / 15.f));
+  if (__builtin_fmaf(15.f, h2f(s), t.lo) > 65504.f) --s;  // the FP16 below (s > 0 here)
+  t.s = h2f(s);
+  const float y = __builtin_amdgcn_rcpf(t.s);  // 1 ulp; s is 2^-24 or more, or 0
+  t.inv = s == 0 || bad ? 0.f : __builtin_fmaf(__builtin_fmaf(-t.s, y, 1.f), y, y);
+  t.s16 = bad ? (uint16_t)0x7E00u : s;
+  if (bad) t.lo16 = 0;
+  return t;
+}
+// min(rint(fp32((v - lo) / s)), 15) in the low bits of a float's bits: adding 1.5 2^23 rounds to an integer, to even.
+__device__ __forceinline__ uint32_t code(const Step& t, uint16_t h) {
+  const float q = quotient(__builtin_fmaf(h2f(h), 1.f, -t.lo), t.s, t.inv);
+  return __float_as_uint(fminf(q, 15.f) + 12582912.f);
+}
+// The low 16 bits are a + 16 b + 256 c + 4096 d; the upper are not used.
+__device__ __forceinline__ uint32_t nibbles(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return (((((d << 4) + c) << 4) + b) << 4) + a;
+}
+__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return perm(b, a, 0x05040100u); }
+
+template <int D, int NG>
+__device__ __forceinline__ void write_keys(uint8_t* unit, const Rows& k, const UnitTask& x, int h, int lane) {
+  using L = Geo<D, NG>;
+  constexpr int R = L::G / 32;  // runs of a group
+  const int t = lane & 15, kq = lane >> 4, pos = 16 * x.u + t;
+  const bool on = pos >= x.p0 && pos < x.p0 + x.n;
+  uint32_t v[4 * L::ND];
+#pragma unroll
+  for (int i = 0; i < 4 * L::ND; ++i) v[i] = 0;
+  if (on) {
+    const int64_t e = (int64_t)(x.row + pos - x.p0) * k.ts + (int64_t)h * k.hs + 8 * kq;
+#pragma unroll
+    for (int j = 0; j < L::ND; ++j) load_pairs<8>(k, e + 32 * j, v + 4 * j);
+  }
+  Extent m[NG];
+  uint32_t top = 0;
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    m[g] = extent<4 * R>(v + 4 * R * g);
+    m[g].ends = over_column(m[g].ends, pk_min);
+    top = pk_max_u16(top, m[g].top);
+  }
+  const bool some_bad = __ballot(bad_top(top)) != 0;
+  uint32_t w[L::ND];
+  uint16_t ks[NG], kl[NG];
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    const Step st = make_step(m[g].ends, some_bad && bad_top(over_column(m[g].top, pk_max_u16)));
+    ks[g] = st.s16;
+    kl[g] = st.lo16;
+#pragma unroll
+    for (int j = g * R; j < (g + 1) * R; ++j) {  // nibble i + 4 e: dimension 2 i + e of the run
+      uint32_t c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = code(st, (uint16_t)(v[4 * j + i / 2] >> (16 * (i & 1))));
+      w[j] = low_halves(nibbles(c[0], c[2], c[4], c[6]), nibbles(c[1], c[3], c[5], c[7]));
+    }
+  }
+  if (!on) return;
+  uint32_t* to = (uint32_t*)unit + lane * L::ND;
+  if constexpr (L::ND == 2) {
+    *(u32x2_t*)to = (u32x2_t){w[0], w[1]};
+  } else {
+#pragma unroll
+    for (int j = 0; j < L::ND; j += 4) *(u32x4_t*)(to + j) = (u32x4_t){w[j], w[j + 1], w[j + 2], w[j + 3]};
+  }
+#pragma unroll
+  for (int g = 0; g < NG; ++g)
+    if ((g & 3) == kq) {
+      ((uint16_t*)(unit + L::off_ks))[((t >> 2) * NG + g) * 4 + (t & 3)] = ks[g];
+      ((uint16_t*)(unit + L::off_kl))[t * NG + g] = kl[g];
+    }
 }
 
-// Codes of the thread's 8 values and its group's s and lo.
-template <int G>
-__device__ __forceinline__ void quantise(float (&v)[8], uint32_t (&q)[8], uint16_t& s16, uint16_t& lo16) {
-  float lo = INFINITY, hi = -INFINITY, bad = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[i] = h2f(f2h(v[i]));
-    lo = fminf(lo, v[i]);
-    hi = fmaxf(hi, v[i]);
-    bad = fmaxf(bad, not_finite(f2h(v[i])) ? 1.f : 0.f);  // fminf and fmaxf pass a NaN by
-  }
-  float ok = -bad;
-  group_min_max<G / 8>(lo, hi);
-  group_min_max<G / 8>(ok, bad);
-  uint16_t s = f2h((hi - lo) / 15.f);
-  if (lo + 15.f * h2f(s) > 65504.f) --s;  // the FP16 below (s > 0 here)
-  const float sf = h2f(s);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float r = rintf((v[i] - lo) / sf);
-    q[i] = s != 0 && bad == 0.f ? (uint32_t)fminf(fmaxf(r, 0.f), 15.f) : 0u;
-  }
-  s16 = bad != 0.f ? (uint16_t)0x7E00u : s;
-  lo16 = bad != 0.f ? (uint16_t)0u : f2h(lo);
+// Over the 2, 4, 8 or 16 neighbouring lanes of a group.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+  v = settled(v);
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, false);
 }
-
-// Pair layout of 8 values: nibble i + 4 e holds value 2 i + e.
-__device__ __forceinline__ uint32_t pack_pairs(const uint32_t (&q)[8]) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w |= (q[2 * i] << (4 * i)) | (q[2 * i + 1] << (16 + 4 * i));
-  return w;
+template <int N, class Op>
+__device__ __forceinline__ uint32_t over_lanes(uint32_t v, Op op) {
+  v = op(v, dpp_u32<0xB1>(v));                       // i ^ 1
+  if constexpr (N > 2) v = op(v, dpp_u32<0x4E>(v));   // i ^ 2
+  if constexpr (N > 4) v = op(v, dpp_u32<0x141>(v));  // the other four of eight
+  if constexpr (N > 8) v = op(v, dpp_u32<0x140>(v));  // the other eight of sixteen
+  return v;
 }
 
 template <int D, int NG>
-__global__ void __launch_bounds__(256)
-k_qcache_write(uint8_t* __restrict__ cache, Seqs sq, Rows k, Rows v, int heads) {
+__device__ __forceinline__ void write_values(uint8_t* unit, const Rows& v, const UnitTask& x, int h, int lane) {
   using L = Geo<D, NG>;
-  constexpr int C = D / 8;  // threads of a vector
-  const int t = blockIdx.x * (256 / C) + threadIdx.x / C, c = threadIdx.x % C, h = blockIdx.y;
-  int pos = -1, s = -1;
-  if (t < sq.n_tok) s = sq.find(t, pos);
-  const int u = pos >> 4;
-  const int p = s >= 0 && pos >= 0 ? sq.page(s, u) : -1;
-  float kv[8] = {}, vv[8] = {};
-  if (p >= 0) {
-    load8(k, t * k.ts + h * k.hs + 8 * c, kv);
-    load8(v, t * v.ts + h * v.hs + 8 * c, vv);
+  constexpr int DL = D / 16, N = L::G / DL;  // dimensions of a lane, lanes of a group
+  const int m = lane & 15, kq = lane >> 4;
+  uint32_t r[4][DL / 2];
+  bool on[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int pos = 16 * x.u + 4 * kq + i;
+    on[i] = pos >= x.p0 && pos < x.p0 + x.n;
+#pragma unroll
+    for (int j = 0; j < DL / 2; ++j) r[i][j] = 0;
+    if (on[i]) load_pairs<DL>(v, (int64_t)(x.row + pos - x.p0) * v.ts + (int64_t)h * v.hs + DL * m, r[i]);
   }
-  // A vector's lanes share p, so no group is split by it; all lanes take part in the group minima.
-  uint32_t qk[8], qv[8];
-  uint16_t ks, kl, vs, vl;
-  quantise<L::G>(kv, qk, ks, kl);
-  quantise<L::G>(vv, qv, vs, vl);
+  Extent e[4];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    e[i] = extent<DL / 2>(r[i]);
+    e[i].ends = over_lanes<N>(e[i].ends, pk_min);
+    top = pk_max_u16(top, e[i].top);
+  }
+  const bool some_bad = __ballot(bad_top(top)) != 0;
+  uint32_t half[4][L::NC];  // of token i: in the low 16 bits, its dimensions 4 c .. 4 c + 3
+  uint16_t vs[4], vl[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const Step st = make_step(e[i].ends, some_bad && bad_top(over_lanes<N>(e[i].top, pk_max_u16)));
+    vs[i] = st.s16;
+    vl[i] = st.lo16;
+#pragma unroll
+    for (int c = 0; c < L::NC; ++c) {
+      uint32_t q[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) q[k] = code(st, (uint16_t)(r[i][2 * c + k / 2] >> (16 * (k & 1))));
+      half[i][c] = nibbles(q[0], q[1], q[2], q[3]);
+    }
+  }
+  uint32_t* to = (uint32_t*)(unit + L::off_v) + lane * L::ND;
+  uint16_t* stats = (uint16_t*)(unit + L::off_vs) + (kq * NG + m / N) * 8;
+  const bool first = m % N == 0;
+  if (on[0] && on[1] && on[2] && on[3]) {
+    uint32_t w[L::ND];
+#pragma unroll
+    for (int tp = 0; tp < 2; ++tp)
+#pragma unroll
+      for (int c = 0; c < L::NC; ++c) w[tp * L::NC + c] = low_halves(half[2 * tp][c], half[2 * tp + 1][c]);
+    if constexpr (L::ND == 2) {
+      *(u32x2_t*)to = (u32x2_t){w[0], w[1]};
+    } else {
+#pragma unroll
+      for (int j = 0; j < L::ND; j += 4) *(u32x4_t*)(to + j) = (u32x4_t){w[j], w[j + 1], w[j + 2], w[j + 3]};
+    }
+    if (first) {
+      auto two = [](uint16_t a, uint16_t b) { return (uint32_t)a | ((uint32_t)b << 16); };
+      *(u32x4_t*)stats = (u32x4_t){two(vs[0], vs[1]), two(vs[2], vs[3]), two(vl[0], vl[1]), two(vl[2], vl[3])};
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (!on[i]) continue;
+#pragma unroll
+    for (int c = 0; c < L::NC; ++c) ((uint16_t*)to)[2 * ((i >> 1) * L::NC + c) + (i & 1)] = (uint16_t)half[i][c];
+    if (first) {
+      stats[i] = vs[i];
+      stats[4 + i] = vl[i];
+    }
+  }
+}
+
+// Four waves a workgroup: two units' keys and values.  Neighbouring workgroups take the heads of the same rows, which
+// are neighbours in memory.
+template <int D, int NG>
+__global__ void __launch_bounds__(256)
+k_qcache_write(uint8_t* __restrict__ cache, Seqs sq, Rows k, Rows v, int heads, Divisor by_heads) {
+  const int pair = by_heads.of(blockIdx.x), h = blockIdx.x - pair * heads;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const UnitTask x = unit_task(sq, pair * 2 + (w >> 1));
+  if (x.s < 0) return;
+  const int p = sq.page(x.s, x.u);
   if (p < 0) return;
-  uint8_t* unit = cache + unit_at(p, u, h, heads, sq.up_shift, L::bytes);
-  const int tk = pos & 15, kq = tk >> 2;
-  // keys: chunk c is step c / 4, slice c % 4
-  ((uint32_t*)unit)[((c & 3) * 16 + tk) * L::ND + (c >> 2)] = pack_pairs(qk);
-  // values: two runs of four dimensions, each a 16-bit half of a dword
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int quad = 2 * c + j, m = quad / L::NC, cc = quad % L::NC;
-    const uint32_t w = qv[4 * j] | (qv[4 * j + 1] << 4) | (qv[4 * j + 2] << 8) | (qv[4 * j + 3] << 12);
-    ((uint16_t*)(unit + L::off_v))[2 * ((kq * 16 + m) * L::ND + ((tk >> 1) & 1) * L::NC + cc) + (tk & 1)] = (uint16_t)w;
-  }
-  if (c % (L::G / 8) == 0) {
-    const int g = c / (L::G / 8);
-    ((uint16_t*)(unit + L::off_ks))[(kq * NG + g) * 4 + (tk & 3)] = ks;
-    ((uint16_t*)(unit + L::off_kl))[tk * NG + g] = kl;
-    ((uint16_t*)(unit + L::off_vs))[(kq * NG + g) * 8 + (tk & 3)] = vs;
-    ((uint16_t*)(unit + L::off_vs))[(kq * NG + g) * 8 + 4 + (tk & 3)] = vl;
-  }
+  uint8_t* unit = cache + unit_at(p, x.u, h, heads, sq.up_shift, Geo<D, NG>::bytes);
+  if (w & 1) write_values<D, NG>(unit, v, x, h, lane);
+  else write_keys<D, NG>(unit, k, x, h, lane);
 }
 
 template <int D, int NG>
 __global__ void __launch_bounds__(256)
-k_qcache_read(const uint8_t* __restrict__ cache, Seqs sq, Rows k, Rows v, int heads) {
+k_qcache_read(const uint8_t* __restrict__ cache, Seqs sq, Rows k, Rows v, int heads, Divisor by_heads) {
   using L = Geo<D, NG>;
-  constexpr int C = D / 8;
-  const int t = blockIdx.x * (256 / C) + threadIdx.x / C, c = threadIdx.x % C, h = blockIdx.y;
-  if (t >= sq.n_tok) return;
-  int pos = -1;
-  const int s = sq.find(t, pos);
-  if (s < 0) return;
-  const int u = pos >> 4;
-  const int p = pos >= 0 ? sq.page(s, u) : -1;
-  float kv[8] = {}, vv[8] = {};
+  const int pair = by_heads.of(blockIdx.x), h = blockIdx.x - pair * heads;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const UnitTask x = unit_task(sq, pair * 2 + (w >> 1));
+  if (x.s < 0) return;
+  const int p = sq.page(x.s, x.u);
+  const uint8_t* unit = cache + unit_at(max(p, 0), x.u, h, heads, sq.up_shift, L::bytes);
+  const int n = lane & 15, kq = lane >> 4;
+  uint32_t c[L::ND];
+#pragma unroll
+  for (int i = 0; i < L::ND; ++i) c[i] = 0;
+  const uint32_t* from = (const uint32_t*)(unit + ((w & 1) ? L::off_v : 0)) + lane * L::ND;
   if (p >= 0) {
-    const uint8_t* unit = cache + unit_at(p, u, h, heads, sq.up_shift, L::bytes);
-    const int tk = pos & 15, kq = tk >> 2, g = c / (L::G / 8);
-    const uint32_t w = ((const uint32_t*)unit)[((c & 3) * 16 + tk) * L::ND + (c >> 2)];
-    const float ks = h2f(((const uint16_t*)(unit + L::off_ks))[(kq * NG + g) * 4 + (tk & 3)]);
-    const float kl = h2f(((const uint16_t*)(unit + L::off_kl))[tk * NG + g]);
-    const float vs = h2f(((const uint16_t*)(unit + L::off_vs))[(kq * NG + g) * 8 + (tk & 3)]);
-    const float vl = h2f(((const uint16_t*)(unit + L::off_vs))[(kq * NG + g) * 8 + 4 + (tk & 3)]);
+    if constexpr (L::ND == 2) {
+      const u32x2_t y = *(const u32x2_t*)from;
+      c[0] = y[0], c[1] = y[1];
+    } else {
+#pragma unroll
+      for (int i = 0; i < L::ND; i += 4) {
+        const u32x4_t y = *(const u32x4_t*)(from + i);
+        c[i] = y[0], c[i + 1] = y[1], c[i + 2] = y[2], c[i + 3] = y[3];
+      }
+    }
+  }
+  if (w & 1) {
+    constexpr int DL = D / 16, N = L::G / DL;
+    u32x4_t st = {0u, 0u, 0u, 0u};
+    if (p >= 0) st = *(const u32x4_t*)(unit + L::off_vs + (kq * NG + n / N) * 16);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      kv[2 * i] = kl + ks * (float)((w >> (4 * i)) & 15u);
-      kv[2 * i + 1] = kl + ks * (float)((w >> (16 + 4 * i)) & 15u);
+      const int pos = 16 * x.u + 4 * kq + i, hs = 16 * (i & 1);
+      if (pos < x.p0 || pos >= x.p0 + x.n) continue;
+      const float s = h2f((uint16_t)(st[i / 2] >> hs)), lo = h2f((uint16_t)(st[2 + i / 2] >> hs));
+      float o[DL];
+#pragma unroll
+      for (int j = 0; j < DL; ++j) o[j] = lo + s * (float)((c[(i >> 1) * L::NC + j / 4] >> (hs + 4 * (j & 3))) & 15u);
+      store_values<DL>(v, (int64_t)(x.row + pos - x.p0) * v.ts + (int64_t)h * v.hs + DL * n, o);
     }
+  } else {
+    const int pos = 16 * x.u + n;
+    if (pos < x.p0 || pos >= x.p0 + x.n) return;
+    const int64_t e = (int64_t)(x.row + pos - x.p0) * k.ts + (int64_t)h * k.hs + 8 * kq;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int quad = 2 * c + j, m = quad / L::NC, cc = quad % L::NC;
-      const uint32_t x =
-          ((const uint16_t*)(unit + L::off_v))[2 * ((kq * 16 + m) * L::ND + ((tk >> 1) & 1) * L::NC + cc) + (tk & 1)];
+    for (int g = 0; g < NG; ++g) {
+      float s = 0.f, lo = 0.f;
+      if (p >= 0) {
+        s = h2f(((const uint16_t*)(unit + L::off_ks))[((n >> 2) * NG + g) * 4 + (n & 3)]);
+        lo = h2f(((const uint16_t*)(unit + L::off_kl))[n * NG + g]);
+      }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) vv[4 * j + i] = vl + vs * (float)((x >> (4 * i)) & 15u);
+      for (int j = g * (L::G / 32); j < (g + 1) * (L::G / 32); ++j) {
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = lo + s * (float)((c[j] >> (16 * (i & 1) + 4 * (i / 2))) & 15u);
+        store_values<8>(k, e + 32 * j, o);
+      }
     }
   }
-  store8(k, t * k.ts + h * k.hs + 8 * c, kv);
-  store8(v, t * v.ts + h * v.hs + 8 * c, vv);
 }
 
 // ---------------------------------------------------------------------------
@@ -269,19 +536,6 @@ k_qcache_read(const uint8_t* __restrict__ cache, Seqs sq, Rows k, Rows v, int he
 // workgroup leaves a partial (at most two per workgroup: the item it starts in,
 // slot 0, and the one it ends in, slot 1), and k_qcache_join adds them in order.
 // ---------------------------------------------------------------------------
-// x / d for 0 <= x < 2^31 as a multiplication: M = 2^(31 + sh) / d + 1, 2^(sh - 1) < d <= 2^sh.
-struct Divisor {
-  uint32_t d, mul, sh;
-  __device__ __forceinline__ int of(int x) const {
-    return d == 1 ? x : (int)(__umulhi((uint32_t)x, mul) >> (sh - 1));
-  }
-};
-inline Divisor divisor(int d) {
-  uint32_t sh = 0;
-  while ((1u << sh) < (uint32_t)d) ++sh;
-  return Divisor{(uint32_t)d, (uint32_t)((((uint64_t)1 << (31 + sh)) / (uint32_t)d) + 1), sh};
-}
-
 // How `total` blocks are cut into `grid` ranges: the first rem have q + 1, the others q.
 struct Cut {
   int q, rem;
@@ -338,27 +592,6 @@ __device__ __forceinline__ int wave_scan(int v) {  // inclusive
   v = dpp_add<0x142, 0xA>(v);  // lane 15 of rows 0, 2 to rows 1, 3
   return dpp_add<0x143, 0xC>(v);  // lane 31 to rows 2, 3
 }
-
-// Lanes i ^ 16, then i ^ 32: each swap leaves the two partners' values in x and y.
-template <class Op>
-__device__ __forceinline__ float over_column(float v, Op op) {  // the four lanes of a column
-  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = op(__uint_as_float(a[0]), __uint_as_float(a[1]));
-  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return op(__uint_as_float(b[0]), __uint_as_float(b[1]));
-}
-__device__ __forceinline__ float column_max(float v) {
-  return over_column(v, [](float x, float y) { return fmaxf(x, y); });
-}
-__device__ __forceinline__ float column_sum(float v) {
-  return over_column(v, [](float x, float y) { return x + y; });
-}
-
-typedef float floatx2_t __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t pk_h(float a, float b) {  // round to nearest even
-  return as_u32(__builtin_convertvector((floatx2_t){a, b}, half2_t));
-}
-__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }  // 1 ulp; results below 2^-126 are 0
 
 // The same value, unknown to the compiler: what is computed from it stays where it is written, instead of being
 // kept in registers across a loop that has none to spare.
@@ -936,6 +1169,7 @@ int check_shape(const qcache_shape* sh) {
 
 int check_counts(const qcache_shape* sh, const qcache_seqs* sq) {
   if (!sq || sq->n_seq < 0 || sq->n_tok < 0 || sq->max_pages < 0) return QGEMV_ERR_INVALID_ARG;
+  if (sq->n_seq > 1 << 28) return QGEMV_ERR_UNSUPPORTED;
   if ((int64_t)sq->max_pages * sh->page_size > 0x7FFFFFFF - 1024) return QGEMV_ERR_UNSUPPORTED;
   return QGEMV_OK;
 }
@@ -987,17 +1221,15 @@ hipError_t by_shape(const qcache_shape* sh, F f) {
 template <int D, int NG>
 hipError_t launch_write(Dims<D, NG>, uint8_t* cache, const Seqs& sq, const Rows& k, const Rows& v, int heads,
                         hipStream_t st) {
-  const int per = 256 / (D / 8);
-  hipLaunchKernelGGL((k_qcache_write<D, NG>), dim3((sq.n_tok + per - 1) / per, heads), dim3(256), 0, st, cache, sq, k, v,
-                     heads);
+  hipLaunchKernelGGL((k_qcache_write<D, NG>), dim3((unit_waves(sq) + 1) / 2 * heads), dim3(256), 0, st, cache, sq, k, v,
+                     heads, divisor(heads));
   return hipGetLastError();
 }
 template <int D, int NG>
 hipError_t launch_read(Dims<D, NG>, const uint8_t* cache, const Seqs& sq, const Rows& k, const Rows& v, int heads,
                        hipStream_t st) {
-  const int per = 256 / (D / 8);
-  hipLaunchKernelGGL((k_qcache_read<D, NG>), dim3((sq.n_tok + per - 1) / per, heads), dim3(256), 0, st, cache, sq, k, v,
-                     heads);
+  hipLaunchKernelGGL((k_qcache_read<D, NG>), dim3((unit_waves(sq) + 1) / 2 * heads), dim3(256), 0, st, cache, sq, k, v,
+                     heads, divisor(heads));
   return hipGetLastError();
 }
 
@@ -1065,7 +1297,10 @@ static int check_copy(const qcache_shape* shape, const void* cache, const qcache
   if ((st = check_seqs(shape, seqs))) return st;
   if (seqs->n_seq == 0 || seqs->n_tok == 0) return QGEMV_OK;
   if ((st = check_rows(k)) || (st = check_rows(v))) return st;
-  return k->type == v->type ? QGEMV_OK : QGEMV_ERR_INVALID_ARG;
+  if (k->type != v->type) return QGEMV_ERR_INVALID_ARG;
+  // workgroups of a launch
+  if (((int64_t)seqs->n_tok / 32 + seqs->n_seq + 1) * shape->n_heads > 0x7FFFFFFF) return QGEMV_ERR_UNSUPPORTED;
+  return QGEMV_OK;
 }
 
 int qcache_write(const qcache_shape* shape, void* cache, const qcache_seqs* seqs, const qcache_rows* k,
