@@ -21,7 +21,9 @@ from __future__ import annotations
 import ctypes
 import math
 
-from .qgemv import _check, _launch, lib as _qgemv_lib
+import torch
+
+from .qgemv import QgemvError, _check, _launch, _stream_here, lib as _qgemv_lib
 
 
 class Shape(ctypes.Structure):
@@ -75,45 +77,39 @@ class QCache:
     """
 
     def __init__(self, n_pages, n_heads, head_dim, page_size=64, group=32, device="cuda"):
-        import torch
         self.n_pages, self.n_heads, self.head_dim = int(n_pages), int(n_heads), int(head_dim)
         self.page_size, self.group = int(page_size), int(group)
         n = cache_bytes(self.n_pages, self.n_heads, self.head_dim, self.page_size, self.group)
         self.data = torch.empty(n, dtype=torch.uint8, device=device)
         self._shape = Shape(self.n_pages, self.n_heads, self.head_dim, self.page_size, self.group)
 
-    def _seqs(self, lens, pages, q_start, n_tok):
-        import torch
-        dev, i32 = self.data.device, torch.int32
-        if lens.dtype != i32 or lens.dim() != 1 or not lens.is_contiguous():
-            raise ValueError("lens must be a contiguous int32 [S] tensor")
+    def _seqs(self, lens, pages, q_start, n_tok, at):
+        i32 = torch.int32
         S = lens.shape[0]
-        if pages.dtype != i32 or pages.dim() != 2 or pages.shape[0] != S or not pages.is_contiguous():
-            raise ValueError("pages must be a contiguous int32 [S, P] tensor")
-        if lens.device != dev or pages.device != dev:
-            raise ValueError(f"all tensors must be on the cache's device {dev}")
-        start = None
-        if q_start is not None:
-            if q_start.dtype != i32 or tuple(q_start.shape) != (S + 1,) or not q_start.is_contiguous():
-                raise ValueError("q_start must be a contiguous int32 [S + 1] tensor")
-            if q_start.device != dev:
-                raise ValueError(f"all tensors must be on the cache's device {dev}")
-            start = q_start.data_ptr()
-        elif n_tok != S:
-            raise ValueError("without q_start there is one row per sequence")
-        return Seqs(S, n_tok, pages.shape[1], start, lens.data_ptr(), pages.data_ptr())
+        if lens.dtype != i32 or lens.shape != (S,) or not lens.is_contiguous() or lens.get_device() != at:
+            raise ValueError("lens must be a contiguous int32 [S] tensor on the cache's device")
+        P = pages.shape[-1]
+        if pages.dtype != i32 or pages.shape != (S, P) or not pages.is_contiguous() or pages.get_device() != at:
+            raise ValueError("pages must be a contiguous int32 [S, P] tensor on the cache's device")
+        if q_start is None:
+            if n_tok != S:
+                raise ValueError("without q_start there is one row per sequence")
+            return Seqs(S, n_tok, P, None, lens.data_ptr(), pages.data_ptr())
+        if q_start.dtype != i32 or q_start.shape != (S + 1,) or not q_start.is_contiguous() or (
+                q_start.get_device() != at):
+            raise ValueError("q_start must be a contiguous int32 [S + 1] tensor on the cache's device")
+        return Seqs(S, n_tok, P, q_start.data_ptr(), lens.data_ptr(), pages.data_ptr())
 
-    def _rows(self, t, heads, what, types):
-        """A [T, heads, head_dim] tensor as the library takes it; where a stride does not matter it is 0."""
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.head_dim or t.dtype not in types:
-            raise ValueError(f"{what} must be a [T, {heads}, {self.head_dim}] tensor of {types}")
-        ts, hs, ds = t.stride()
-        if ds != 1:
+    def _rows(self, t, heads, what, at):
+        """A [T, heads, head_dim] tensor as the library takes it; a stride that does not matter is 0."""
+        dt, T = t.dtype, t.shape[0]
+        if (dt != torch.float16 and dt != torch.float32) or t.shape != (T, heads, self.head_dim) or (
+                t.get_device() != at):
+            raise ValueError(f"{what} must be an FP16 or fp32 [T, {heads}, {self.head_dim}] tensor on the cache's device")
+        ts, hs, one = t.stride()
+        if one != 1:
             raise ValueError(f"{what}: the last dimension must be contiguous")
-        if t.device != self.data.device:
-            raise ValueError(f"all tensors must be on the cache's device {self.data.device}")
-        return Rows(t.data_ptr(), 0 if t.element_size() == 2 else 1, ts if t.shape[0] > 1 else 0,
-                    hs if heads > 1 else 0)
+        return Rows(t.data_ptr(), dt == torch.float32, ts if T > 1 else 0, hs if heads > 1 else 0)
 
     def write(self, k, v, lens, pages, q_start=None, stream=None):
         """Quantise the rows of k and v [T, n_heads, head_dim] (both FP16 or both fp32) into their positions.
@@ -121,14 +117,18 @@ class QCache:
         k and v may be views with strides that are multiples of 8 elements (columns of a stacked q/k/v
         product), starting on 16 bytes.
         """
-        import torch
-        if v.shape != k.shape or v.dtype != k.dtype:
+        at = self.data.get_device()
+        s = _stream_here(at, stream)
+        if s is None:
+            with _launch(at, stream):
+                return self.write(k, v, lens, pages, q_start)
+        kr, vr = self._rows(k, self.n_heads, "k", at), self._rows(v, self.n_heads, "v", at)
+        if v.shape[0] != k.shape[0] or kr.type != vr.type:
             raise ValueError("k and v must have the same shape and type")
-        types = (torch.float16, torch.float32)
-        kr, vr = self._rows(k, self.n_heads, "k", types), self._rows(v, self.n_heads, "v", types)
-        sq = self._seqs(lens, pages, q_start, k.shape[0])
-        with _launch(self.data.device, stream) as s:
-            _check(lib().qcache_write(self._shape, self.data.data_ptr(), sq, kr, vr, s), "qcache_write")
+        sq = self._seqs(lens, pages, q_start, k.shape[0], at)
+        st = lib().qcache_write(self._shape, self.data.data_ptr(), sq, kr, vr, s)
+        if st != 0:
+            raise QgemvError(st, "qcache_write")
 
     def read(self, lens, pages, q_start=None, n_tok=None, k=None, v=None, dtype=None, stream=None):
         """(k, v): the values held where write() would have put the rows, [n_tok, n_heads, head_dim].
@@ -136,26 +136,32 @@ class QCache:
         Allocated as dtype (FP16 by default) if k and v are not given; rows of padding are then not
         initialised.  n_tok: rows of the outputs, by default those of k, or one per sequence.
         """
-        import torch
-        types = (torch.float16, torch.float32)
-        if (k is None) != (v is None):
+        at = self.data.get_device()
+        s = _stream_here(at, stream)
+        if s is None:
+            with _launch(at, stream):
+                return self.read(lens, pages, q_start, n_tok, k, v, dtype)
+        if k is None and v is None:
+            if n_tok is None:
+                if q_start is not None:
+                    raise ValueError("with q_start the number of rows must be given: n_tok, or k and v")
+                n_tok = lens.shape[0]
+            if dtype is None:
+                dtype = torch.float16
+            elif dtype != torch.float16 and dtype != torch.float32:
+                raise ValueError("dtype must be torch.float16 or torch.float32")
+            k, v = torch.empty((2, n_tok, self.n_heads, self.head_dim), dtype=dtype, device=self.data.device).unbind(0)
+        elif k is None or v is None:
             raise ValueError("give both k and v, or neither")
-        if n_tok is None:
-            n_tok = k.shape[0] if k is not None else lens.shape[0]
-            if k is None and q_start is not None:
-                raise ValueError("with q_start the number of rows must be given: n_tok, or k and v")
-        if dtype is not None and (dtype not in types or (k is not None and k.dtype != dtype)):
-            raise ValueError("dtype must be torch.float16 or torch.float32, and that of k and v")
-        if k is not None and (k.shape != v.shape or k.dtype != v.dtype or k.shape[0] != n_tok):
+        elif dtype is not None and dtype != k.dtype:
+            raise ValueError("dtype is not that of k and v")
+        kr, vr = self._rows(k, self.n_heads, "k", at), self._rows(v, self.n_heads, "v", at)
+        if v.shape[0] != k.shape[0] or kr.type != vr.type or n_tok not in (None, k.shape[0]):
             raise ValueError("k and v must have the same shape and type, and n_tok rows")
-        sq = self._seqs(lens, pages, q_start, n_tok)
-        with _launch(self.data.device, stream) as s:
-            if k is None:
-                shape = (n_tok, self.n_heads, self.head_dim)
-                k = torch.empty(shape, dtype=dtype or types[0], device=self.data.device)
-                v = torch.empty(shape, dtype=dtype or types[0], device=self.data.device)
-            kr, vr = self._rows(k, self.n_heads, "k", types), self._rows(v, self.n_heads, "v", types)
-            _check(lib().qcache_read(self._shape, self.data.data_ptr(), sq, kr, vr, s), "qcache_read")
+        sq = self._seqs(lens, pages, q_start, k.shape[0], at)
+        st = lib().qcache_read(self._shape, self.data.data_ptr(), sq, kr, vr, s)
+        if st != 0:
+            raise QgemvError(st, "qcache_read")
         return k, v
 
     def attend(self, q, lens, pages, q_start=None, scale=None, out=None, stream=None):
@@ -165,24 +171,34 @@ class QCache:
         scale: 1 / sqrt(head_dim) by default.  out: FP16, the shape of q, allocated if not given (rows of
         padding are then not initialised); it must not overlap q.  A row that sees nothing is 0.
         """
-        import torch
-        if q.dim() != 3 or q.shape[1] < 1 or q.shape[1] % self.n_heads:
-            raise ValueError(f"q must be [T, heads, {self.head_dim}] with a multiple of {self.n_heads} heads")
-        H = q.shape[1]
-        qr = self._rows(q, H, "q", (torch.float16,))
-        sq = self._seqs(lens, pages, q_start, q.shape[0])
-        scale = 1.0 / math.sqrt(self.head_dim) if scale is None else float(scale)
-        if not math.isfinite(scale):
+        at = self.data.get_device()
+        s = _stream_here(at, stream)
+        if s is None:
+            with _launch(at, stream):
+                return self.attend(q, lens, pages, q_start, scale, out)
+        if q.dim() != 3 or q.shape[1] < 1 or q.shape[1] % self.n_heads or q.dtype != torch.float16:
+            raise ValueError(f"q must be FP16 [T, heads, {self.head_dim}] with a multiple of {self.n_heads} heads")
+        T, H = q.shape[0], q.shape[1]
+        qr = self._rows(q, H, "q", at)
+        sq = self._seqs(lens, pages, q_start, T, at)
+        if scale is None:
+            scale = 1.0 / math.sqrt(self.head_dim)
+        elif not math.isfinite(scale):
             raise ValueError("scale must be finite")
-        if out is not None and out.shape != q.shape:
-            raise ValueError("out must have the shape of q")
+        if out is None:
+            out = torch.empty((T, H, self.head_dim), dtype=torch.float16, device=self.data.device)
+            orow = Rows(out.data_ptr(), 0, H * self.head_dim, self.head_dim)
+        else:
+            if out.shape != q.shape or out.dtype != torch.float16:
+                raise ValueError("out must be FP16 in the shape of q")
+            orow = self._rows(out, H, "out", at)
         n = ctypes.c_size_t(0)
-        _check(lib().qcache_attend_ws(self._shape, sq, H, n), "qcache_attend_ws")
-        with _launch(self.data.device, stream) as s:
-            if out is None:
-                out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
-            orow = self._rows(out, H, "out", (torch.float16,))
-            ws = torch.empty(n.value, dtype=torch.uint8, device=q.device)
-            _check(lib().qcache_attend(self._shape, self.data.data_ptr(), sq, H, qr, orow, scale, ws.data_ptr(),
-                                       n.value, s), "qcache_attend")
+        L = lib()
+        st = L.qcache_attend_ws(self._shape, sq, H, n)
+        if st == 0:
+            # its own for every call: calls on other streams, and captured ones, never share it
+            ws = torch.empty(n.value, dtype=torch.uint8, device=self.data.device)
+            st = L.qcache_attend(self._shape, self.data.data_ptr(), sq, H, qr, orow, scale, ws.data_ptr(), n.value, s)
+        if st != 0:
+            raise QgemvError(st, "qcache_attend")
         return out

@@ -103,28 +103,28 @@ def lib() -> ctypes.CDLL:
     return L
 
 
-class _launch:
-    """The HIP stream to launch on, with `dev` current and, if a stream is given, that stream current too
-    (so that what is allocated inside belongs to it).  Does nothing where both already hold."""
+def _stream_here(index: int, stream):
+    """The HIP stream to launch on where the device `index` is current and no stream is asked for, else None."""
+    import torch
+    if stream is None and torch._C._cuda_getDevice() == index:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return None
 
-    def __init__(self, dev, stream):
-        self.dev, self.stream, self.ctx = dev, stream, None
+
+class _launch:
+    """Makes the device `index` current, and `stream` if one is given, so that what is allocated inside belongs to it."""
+
+    def __init__(self, index: int, stream):
+        import torch
+        if stream is not None and stream.device.index != index:
+            raise ValueError(f"the stream must be on device {index}")
+        self.ctx = torch.cuda.device(index) if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):
-        import torch
-        if self.stream is not None:
-            if self.stream.device != self.dev:
-                raise ValueError(f"the stream must be on the device {self.dev}")
-            self.ctx = torch.cuda.stream(self.stream)
-        elif self.dev.index is not None and torch.cuda.current_device() != self.dev.index:
-            self.ctx = torch.cuda.device(self.dev)
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return (self.stream or torch.cuda.current_stream(self.dev)).cuda_stream
+        self.ctx.__enter__()
 
     def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+        self.ctx.__exit__(*exc)
         return False
 
 
@@ -297,45 +297,57 @@ class QGemv:
         workspace and must not overlap, and the first must not be captured into a graph.
         """
         import torch
-        dev = self.blob.device
+        at = self.blob.get_device()
+        s = _stream_here(at, stream)
+        if s is None:
+            with _launch(at, stream):
+                return self.run_epilogue(x, bias, act, gated, residual, out, dtype)
         f16, f32 = torch.float16, torch.float32
         if x.dim() == 1:
             x = x.unsqueeze(0)
-        if x.dim() != 2 or x.dtype != f16 or not x.is_contiguous() or x.shape[1] != self.K:
-            raise ValueError("x must be a contiguous FP16 [B, K] tensor")
+        B = x.shape[0]
+        if x.dtype != f16 or x.shape != (B, self.K) or not x.is_contiguous() or x.get_device() != at:
+            raise ValueError("x must be a contiguous FP16 [B, K] tensor on the plan's device")
         if act not in ACT:
             raise ValueError(f"act must be one of {sorted(ACT)}")
-        B = x.shape[0]
         mo = self.M // 2 if gated else self.M
         e = Epilogue()
         e.act, e.gated = ACT[act], bool(gated)
         if bias is not None:
-            if bias.dtype not in (f16, f32) or not bias.is_contiguous() or tuple(bias.shape) != (self.M,):
-                raise ValueError("bias must be a contiguous FP16 or fp32 [M] tensor")
-            e.bias, e.bias_type = bias.data_ptr(), int(bias.dtype == f32)
+            bt = bias.dtype
+            if (bt != f16 and bt != f32) or bias.shape != (self.M,) or not bias.is_contiguous() or (
+                    bias.get_device() != at):
+                raise ValueError("bias must be a contiguous FP16 or fp32 [M] tensor on the plan's device")
+            e.bias, e.bias_type = bias.data_ptr(), bt == f32
         if residual is not None:
-            if residual.dtype not in (f16, f32) or tuple(residual.shape) != (B, mo) or residual.stride(1) != 1 or (
-                    B > 1 and residual.stride(0) < mo):
-                raise ValueError("residual must be an FP16 or fp32 [B, outputs] tensor with contiguous rows")
-            e.residual, e.residual_type = residual.data_ptr(), int(residual.dtype == f32)
-            e.ldr = residual.stride(0) if B > 1 else 0
-        if out is not None:
-            if out.dtype not in (f16, f32) or tuple(out.shape) != (B, mo) or out.stride(1) != 1 or (
-                    B > 1 and out.stride(0) < mo) or (dtype is not None and dtype != out.dtype):
-                raise ValueError("out must be an FP16 or fp32 [B, outputs] tensor with contiguous rows")
-            e.ldy = out.stride(0) if B > 1 else 0
-        elif dtype not in (None, f16, f32):
-            raise ValueError("dtype must be torch.float16 or torch.float32")
-        for t in (x, bias, residual, out):
-            if t is not None and t.device != dev:
-                raise ValueError(f"all tensors must be on the plan's device {dev}")
-        with _launch(dev, stream) as s:
-            if out is None:
-                out = torch.empty((B, mo), dtype=dtype or f16, device=dev)
-            e.y_type = int(out.dtype == f32)
-            _check(lib().qgemv_run_epilogue(self._h, x.data_ptr(), out.data_ptr(), B, ctypes.byref(e), s),
-                   "qgemv_run_epilogue")
+            e.residual, e.residual_type, e.ldr = self._output_rows(residual, B, mo, at, "residual")
+        if out is None:
+            if dtype is None:
+                dtype = f16
+            elif dtype != f16 and dtype != f32:
+                raise ValueError("dtype must be torch.float16 or torch.float32")
+            out = torch.empty((B, mo), dtype=dtype, device=self.blob.device)
+            y, e.y_type = out.data_ptr(), dtype == f32
+        else:
+            if dtype is not None and dtype != out.dtype:
+                raise ValueError("dtype is not that of out")
+            y, e.y_type, e.ldy = self._output_rows(out, B, mo, at, "out")
+        st = lib().qgemv_run_epilogue(self._h, x.data_ptr(), y, B, e, s)
+        if st != 0:
+            raise QgemvError(st, "qgemv_run_epilogue")
         return out
+
+    @staticmethod
+    def _output_rows(t, B, mo, at, what):
+        """(pointer, is fp32, row stride) of an output-shaped tensor with contiguous rows."""
+        import torch
+        f32 = t.dtype == torch.float32
+        if (not f32 and t.dtype != torch.float16) or t.shape != (B, mo) or t.get_device() != at:
+            raise ValueError(f"{what} must be an FP16 or fp32 [B, outputs] tensor on the plan's device")
+        ld, one = t.stride()
+        if one != 1 or (B > 1 and ld < mo):
+            raise ValueError(f"{what} must have contiguous rows that do not overlap")
+        return t.data_ptr(), f32, ld if B > 1 else 0
 
     def debug_unpack(self, stream=None):
         import torch
