@@ -23,6 +23,12 @@ With the default workload the line also carries `targets`: both batch-1
 shapes that have a 70 %-of-8-TB/s target (28672x8192 LUT-4 and 11008x4096
 LUT-3), each next to a plain streaming read of the same number of bytes.
 
+--step-ctx N times one token step of the whole 7B decoder block instead
+(block7b_u3 at --batch sequences of N cached tokens each): the stacked q/k/v
+product, the write of its keys and values into the 4-bit cache, attention
+over it, the output product added to the residual stream, the gated gate/up
+product and the down product added to the residual stream.
+
 --copy-mb N also times a plain elementwise copy of N MiB (a kernel of known
 traffic, used to calibrate the HBM byte counters of a profiler run).
 --trace-summary CSV prints median / p10 / p90 of the timed replays' launches
@@ -366,6 +372,73 @@ def measure(torch, qgemv, workload, B, steps, warmup, rotate_gib, stream, dev, u
     return per_layer, alg_total, ms_total, cpu_layers
 
 
+HEADS_7B, HEAD_DIM_7B = 32, 128  # 4096 activations
+
+
+def step_weights(qgemv):
+    """The 7B block's four products of a step: q/k/v stacked, o, gate/up interleaved, down."""
+    f = {name: format_inputs("block7b_u3", i) for i, name in workload_layers("block7b_u3")}
+    return {"qkv": stack_rows([f["q"], f["k"], f["v"]]), "o": f["o"],
+            "gate_up": qgemv.interleave_rows(f["gate"], f["up"]), "down": f["down"]}
+
+
+def step_bytes(weights: dict, B: int, ctx: int, group: int) -> int:
+    """Algorithmic bytes of a step: every weight set and the cached keys and values once, and the FP16
+    activations between the operators (one write and one read each; algorithmic_bytes counts fp32 y)."""
+    n = sum(algorithmic_bytes(w, B) - 2 * B * w["M"] for w in weights.values()) - 2 * B * weights["gate_up"]["M"] // 2
+    per_token = 2 * HEADS_7B * (HEAD_DIM_7B // 2 + 4 * HEAD_DIM_7B // group)
+    E = HEADS_7B * HEAD_DIM_7B
+    # the cache: read by attention, the new tokens written; q/k/v read by both, its output written; two residuals
+    return n + B * (ctx + 1) * per_token + B * 2 * (3 * E + E + 2 * E)
+
+
+def measure_step(torch, qgemv, B, ctx, steps, warmup, rotate_gib, stream, dev, use_graph):
+    """(ms per step, algorithmic bytes, copies) of the 7B decoder block's token step."""
+    from dense_sparse_bit_amd import qcache
+    from synth import make_x
+    H, D, page, group = HEADS_7B, HEAD_DIM_7B, 64, 32
+    E = H * D
+    weights = step_weights(qgemv)
+    blobs = {n: qgemv.repack(w) for n, w in weights.items()}
+    n_pages = -(-ctx // page)
+    per_copy = sum(b.size for b in blobs.values()) + qcache.cache_bytes(B * n_pages, H, D, page, group)
+    copies = max(2, math.ceil(rotate_gib * (1 << 30) / per_copy))
+    lens = torch.full((B,), ctx, dtype=torch.int32, device=dev)
+    pages = torch.arange(B * n_pages, dtype=torch.int32, device=dev).view(B, n_pages)
+    # a block's norms stand in front of its products; without them, inputs this small keep FP16 finite
+    x = torch.from_numpy(make_x("block7b_u3", B, E)).to(dev) * 0.02
+    plans, caches = [], []
+    k, v = (torch.randn((ctx, H, D), device=dev).half() for _ in range(2))
+    start = torch.tensor([0, ctx], dtype=torch.int32, device=dev)
+    for _ in range(copies):
+        plans.append({n: qgemv.QGemv(weights[n], device="cuda:0", blob=b) for n, b in blobs.items()})
+        caches.append(qcache.QCache(B * n_pages, H, D, page_size=page, group=group, device="cuda:0"))
+        for s in range(B):  # every sequence holds the same keys and values
+            caches[-1].write(k, v, lens[:1], pages[s:s + 1], start)
+    out = [torch.empty_like(x) for _ in range(copies)]
+
+    def step(i):
+        i %= copies
+        p, c = plans[i], caches[i]
+        qkv = p["qkv"].run_epilogue(x)
+        q, kn, vn = (t.unflatten(1, (H, D)) for t in qkv.split(E, dim=1))
+        c.write(kn, vn, lens, pages)
+        h = p["o"].run_epilogue(c.attend(q, lens, pages).view(B, E), residual=x)
+        m = p["gate_up"].run_epilogue(h, act="silu", gated=True)
+        p["down"].run_epilogue(m, residual=h, out=out[i])
+
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):  # a plan's first batched run allocates its workspace: not under capture
+        for i in range(copies):
+            step(i)
+    torch.cuda.synchronize()
+    ms = time_graph(torch, step, steps, warmup, stream, use_graph=use_graph)
+    for y in out:
+        assert torch.isfinite(y).all().item(), "non-finite output"
+        assert torch.equal(y, out[0]), "copies disagree"
+    return ms, step_bytes(weights, B, ctx, group), copies
+
+
 def read_floor(torch, qgemv, nbytes, steps, warmup, stream, dev):
     """µs of one plain streaming read of nbytes (the library's read probe over
     distinct windows of a 2 GiB buffer, one graph replay)."""
@@ -521,6 +594,8 @@ def main():
     ap.add_argument("--layer", default=None, help="only this layer (or fused group) of a multi-layer workload")
     ap.add_argument("--fuse", action="store_true",
                     help="run the layers that share x (q,k,v; gate,up) as one product over their stacked rows")
+    ap.add_argument("--step-ctx", type=int, default=0, metavar="N",
+                    help="time a token step of the whole 7B decoder block over N cached tokens per sequence")
     ap.add_argument("--counter-table", default=None, metavar="CSV",
                     help="only print per-kernel median counters of a rocprofv3 counter run (no GPU)")
     ap.add_argument("--counter-summary", nargs=2, default=None, metavar=("FETCH_CSV", "WRITE_CSV"),
@@ -557,6 +632,23 @@ def main():
         w = int(a.read_probe_mb * 1e6) // 16 * 16
         print(json.dumps({"read_probe": {"bytes": w, "us": round(us, 3), "GBs": round(w / (us * 1e-6) / 1e9, 1)}}),
               flush=True)
+        return
+
+    if a.step_ctx:
+        B = a.batch or DEFAULT_BATCH["block7b_u3"]
+        ms, alg, copies = measure_step(torch, qgemv, B, a.step_ctx, a.steps, a.warmup, a.rotate_gib, stream, dev,
+                                       not a.no_graph)
+        gbs = alg / (ms * 1e-3) / 1e9
+        print(json.dumps({
+            "metric": "µs per token step of a 7B decoder block and effective GB/s as % of MI355X HBM peak",
+            "value": round(gbs, 1), "unit": "GB/s", "us_per_step": round(ms * 1e3, 3),
+            "pct_of_hbm_peak": round(100.0 * gbs / HBM_PEAK_GBS, 2), "n_gpus": 1, "steps": a.steps,
+            "warmup": a.warmup, "ms_per_step": round(ms, 6), "higher_is_better": True, "scaling": "weak",
+            "vs_baseline": None, "dtype": "fp16", "data": "synthetic",
+            "config": {"workload": f"block7b_u3 token step: {WORKLOAD_NOTES['block7b_u3']}; 4-bit cache of {HEADS_7B} "
+                                   f"heads x {HEAD_DIM_7B}, groups of 32, {a.step_ctx} tokens per sequence, batch {B}",
+                       "batch": B, "context": a.step_ctx, "copies_rotated": copies,
+                       "algorithmic_bytes_per_step": alg}}), flush=True)
         return
 
     per_layer, alg_total, ms_total, cpu_layers = measure(torch, qgemv, a.workload, B, a.steps, a.warmup,
