@@ -554,7 +554,7 @@ struct AttendArgs {
   uint16_t* out;
   int64_t q_ts, q_hs, o_ts, o_hs;
   float* ws_o;   // [grid][2][rows][D]
-  float* ws_ml;  // [grid][2][rows][2]: m (log2), sum
+  float* ws_ml;  // [grid][2][rows][4]: m, sum, k_l (m's unit), -
   int* ws_join;  // [grid][4]: last workgroup of the item that this one ends in (-1: none), its first row, item, rows
   int heads, per, rows, grid;
   int whole;  // ranges are cut between items only: every item is one workgroup's
@@ -760,7 +760,7 @@ constexpr int attend_resident(int D) { return D == 256 ? 2 : D == 128 ? 3 : 4; }
 
 template <int D, int NG>
 constexpr int attend_lds() {  // the waves' tiles; then, over them, their O, m and sums
-  const int ring = 4 * 2 * 2 * Geo<D, NG>::bytes, meet = 4 * 16 * (D + 4) * 4 + 2 * 4 * 16 * 4;
+  const int ring = 4 * 2 * 2 * Geo<D, NG>::bytes, meet = 4 * 16 * (D + 4) * 4 + (2 * 4 + 1) * 16 * 4;
   return ring > meet ? ring : meet;
 }
 
@@ -773,6 +773,7 @@ k_qcache_attend(AttendArgs a) {
   float(*s_o)[16][D + 4] = (float(*)[16][D + 4])lds;
   float(*s_m)[16] = (float(*)[16])(lds + 4 * 16 * (D + 4) * 4);
   float(*s_l)[16] = s_m + 4;
+  float* s_k = s_l[4];
   const int lane = threadIdx.x & 63, n = lane & 15, kq = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint8_t* ring = lds + w * (4 * L::bytes);  // two tiles
@@ -910,8 +911,8 @@ k_qcache_attend(AttendArgs a) {
         for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf((float)qv[j][i]));
       top = column_max(top);
       const int e = top > 0.f && top <= 65504.f ? 6 - ilogbf(top) : 0;
-      // never 0, and 8 / k_l finite: both meet infinities below
-      k_l = fmaxf(ldexpf(fabsf(a.scale2), -e), 1e-37f);
+      // never 0 nor infinite, and 8 / k_l finite: all meet infinities below
+      k_l = fminf(fmaxf(ldexpf(fabsf(a.scale2), -e), 1e-37f), 1e30f);
       raise = 8.f / k_l;
       const float up = a.scale2 < 0.f ? -ldexpf(1.f, e) : ldexpf(1.f, e);
 #pragma unroll
@@ -939,7 +940,7 @@ k_qcache_attend(AttendArgs a) {
     floatx4_t o[DL];
 #pragma unroll
     for (int j = 0; j < DL; ++j) o[j] = (floatx4_t){0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, mk = 0.f, l = 0.f;  // m in units of k_l, k_l m (0 while m is -inf), sum of p
+    float m = -INFINITY, mu = 0.f, l = 0.f;  // m in units of k_l; m, but 0 while it is -inf; sum of p
 
     for (int j = 0; j < nt; ++j) {
       const int base = 128 * (k0 + j) + 32 * w;
@@ -971,7 +972,7 @@ k_qcache_attend(AttendArgs a) {
         const float mn = fmaxf(m, column_max(top));
         const float f = mn == m ? 1.f : exp2_(k_l * (m - mn));
         m = mn;
-        mk = mn == -INFINITY ? 0.f : k_l * mn;
+        mu = mn == -INFINITY ? 0.f : mn;
         l *= f;
 #pragma unroll
         for (int j2 = 0; j2 < DL; ++j2) o[j2] *= f;
@@ -982,7 +983,8 @@ k_qcache_attend(AttendArgs a) {
         float p[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          p[i] = exp2_(k_l * st[e][i] - mk);
+          // the difference first: exact near the maximum, and 1 there, however large the scores are
+          p[i] = exp2_(k_l * (st[e][i] - mu));
           l += p[i];
         }
         pf[2 * e] = pk_h(p[0], p[1]);
@@ -1051,7 +1053,8 @@ k_qcache_attend(AttendArgs a) {
     if (real) {
       const int c = tid & 15, k4 = (tid >> 4) & 3;
       if (k4 == 0) {
-        s_m[w][c] = m == -INFINITY ? m : mk;
+        s_m[w][c] = m;
+        if (w == 0) s_k[c] = k_l;
         s_l[w][c] = l;
       }
 #pragma unroll
@@ -1071,7 +1074,7 @@ k_qcache_attend(AttendArgs a) {
       floatx4_t v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const float f = exp2_(s_m[u][row] - mu);
+        const float f = exp2_(s_k[row] * (s_m[u][row] - mu));
         sum += f * s_l[u][row];
         v += f * *(const floatx4_t*)&s_o[u][row][d];
       }
@@ -1084,8 +1087,7 @@ k_qcache_attend(AttendArgs a) {
         const int64_t slot = ((int64_t)blockIdx.x * 2 + (k0 > 0 ? 0 : 1)) * a.rows + row;
         *(floatx4_t*)(a.ws_o + slot * D + d) = v;
         if (d == 0) {
-          a.ws_ml[2 * slot] = mx;
-          a.ws_ml[2 * slot + 1] = sum;
+          *(floatx4_t*)(a.ws_ml + 4 * slot) = (floatx4_t){mx, sum, s_k[row], 0.f};
         }
       }
     }
@@ -1118,9 +1120,10 @@ k_qcache_join(AttendArgs a) {
     const bool on = grp < pg && row < nrows;
     float m = -INFINITY, l = 0.f;
     floatx4_t v = {0.f, 0.f, 0.f, 0.f};
+    float k_l = 1.f;  // the same in all of a row's partials
     auto add = [&](float pm, float pl, floatx4_t pv) {
       const float mn = fmaxf(m, pm), mu = mn == -INFINITY ? 0.f : mn;
-      const float f = exp2_(m - mu), pf = exp2_(pm - mu);
+      const float f = exp2_(k_l * (m - mu)), pf = exp2_(k_l * (pm - mu));
       l = f * l + pf * pl;
       v = f * v + pf * pv;
       m = mn;
@@ -1129,7 +1132,8 @@ k_qcache_join(AttendArgs a) {
 #pragma unroll 4
       for (int i = g + grp; i <= last; i += pg) {
         const int64_t slot = ((int64_t)i * 2 + (i == g ? 1 : 0)) * a.rows + row;
-        const floatx2_t ml = *(const floatx2_t*)(a.ws_ml + 2 * slot);
+        const floatx4_t ml = *(const floatx4_t*)(a.ws_ml + 4 * slot);
+        k_l = ml[2];
         add(ml[0], ml[1], *(const floatx4_t*)(a.ws_o + slot * D + d));
       }
     }
@@ -1264,7 +1268,7 @@ int attend_plan(const qcache_shape* sh, const qcache_seqs* sq, int32_t n_q_heads
   const int most = 256 * attend_resident(sh->head_dim);
   p.grid = all < 1 ? 1 : all < most ? (int)all : most;
   p.rows = sq->q_start || per > 16 ? 16 : per;
-  p.bytes = (size_t)p.grid * (2 * (size_t)p.rows * (sh->head_dim + 2) * 4 + 16);
+  p.bytes = (size_t)p.grid * (2 * (size_t)p.rows * (sh->head_dim + 4) * 4 + 16);
   return QGEMV_OK;
 }
 
@@ -1338,7 +1342,8 @@ int qcache_attend(const qcache_shape* shape, const void* cache, const qcache_seq
   AttendPlan p;
   int st = attend_plan(shape, seqs, n_q_heads, p);
   if (st) return st;
-  if (!cache || (uintptr_t)cache % 256 || !std::isfinite(scale)) return QGEMV_ERR_INVALID_ARG;
+  const float scale2 = scale * 1.4426950408889634f;
+  if (!cache || (uintptr_t)cache % 256 || !std::isfinite(scale2)) return QGEMV_ERR_INVALID_ARG;
   if ((st = check_seqs(shape, seqs))) return st;
   if (seqs->n_seq == 0 || seqs->n_tok == 0) return QGEMV_OK;
   if ((st = check_rows(q)) || (st = check_rows(out))) return st;
@@ -1356,7 +1361,7 @@ int qcache_attend(const qcache_shape* shape, const void* cache, const qcache_seq
   a.o_hs = out->head_stride;
   a.ws_o = (float*)ws;
   a.ws_ml = a.ws_o + (size_t)p.grid * 2 * p.rows * shape->head_dim;
-  a.ws_join = (int*)(a.ws_ml + (size_t)p.grid * 2 * p.rows * 2);
+  a.ws_join = (int*)(a.ws_ml + (size_t)p.grid * 2 * p.rows * 4);
   a.heads = shape->n_heads;
   a.per = n_q_heads / shape->n_heads;
   a.rows = p.rows;
@@ -1364,7 +1369,7 @@ int qcache_attend(const qcache_shape* shape, const void* cache, const qcache_seq
   a.whole = p.whole;
   a.by_heads = divisor(a.heads);
   a.by_per = divisor(a.per);
-  a.scale2 = scale * 1.4426950408889634f;
+  a.scale2 = scale2;
   return hip_status(by_shape(shape, [&](auto d) { return launch_attend(d, a, p, (hipStream_t)stream); }));
 }
 

@@ -111,7 +111,7 @@ int qcache_attend_ws(const qcache_shape* shape, const qcache_seqs* seqs, int32_t
  * over the positions p of row t's sequence up to row t's own.  A row with no
  * such position is 0.  q and out are FP16; scores, softmax statistics and sums
  * are fp32, the weights and the values that they multiply FP16.
- * n_q_heads: a multiple of n_heads, at most 65535.  scale: finite.
+ * n_q_heads: a multiple of n_heads, at most 65535.  scale: finite, also times log2 e.
  * ws: device memory, 256-byte aligned, of qcache_attend_ws bytes, contents
  * undefined before and after; calls that may overlap in time need one each.
  * Meant for a step's few rows per sequence; any number is taken, in tiles of

@@ -220,6 +220,24 @@ def test_write_then_read(torch, D, G, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n_seq", [63, 65, 130, 4099])
+def test_write_many_sequences(torch, n_seq):
+    """The search for a wave's sequence, one and two rounds of it; empty sequences and sequences without rows between."""
+    rng = np.random.default_rng(n_seq)
+    lens = rng.integers(0, 40, n_seq).tolist()
+    new = [int(min(n, k)) for n, k in zip(rng.integers(0, 35, n_seq), lens)]
+    b = Batch(torch, lens, new, 16, pad=9, seed=n_seq)
+    D, H = 64, 2
+    k, v = (rng.standard_normal((b.n_tok, H, D)).astype(np.float16) for _ in range(2))
+    say(f"[gpu] cache write, {n_seq} sequences")
+    c = poison(torch, qcache.QCache(b.total, H, D, page_size=16, group=32))
+    c.write(torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), *b.args())
+    got = c.read(*b.args(), n_tok=b.n_tok, dtype=torch.float32)
+    for g, a in zip(got, (k, v)):
+        assert np.array_equal(g.cpu().numpy()[:b.start[-1]], oc.held(a, 32).astype(np.float32)[:b.start[-1]])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("D,G", [(64, 32), (128, 128), (256, 64)])
 def test_write_extremes(torch, D, G):
     rng = np.random.default_rng(5)
@@ -447,6 +465,34 @@ def test_attend_rising_and_falling_scores(torch):
             q[3, 2, 5] = 30000  # 2^20 and more above the others
         say(f"[gpu] attend ramps size={size} scale={scale}")
         check_attend(b, enc, q, c.attend(torch.from_numpy(q).cuda(), *b.args(), scale=scale), scale, f"size {size} scale {scale}")
+
+
+@pytest.mark.gpu
+def test_attend_tiny_and_huge_values(torch):
+    """Steps and values in FP16's subnormal range, and keys near its end; scales that bring the scores back."""
+    D, G, L = 64, 32, 300
+    b = Batch(torch, [L] * 4, [1] * 4, 64, seed=3, one_each=True)
+    sizes = [(1e-5, 1e-5), (1e-6, 1.0), (3000.0, 3000.0), (1.0, 1e-6)]
+    c, enc = fill(torch, b, 2, D, G, seed=6, keys=lambda s, k: (k.astype(np.float64) * sizes[s][0]).astype(np.float16),
+                  vals=lambda s, v: (v.astype(np.float64) * sizes[s][1]).astype(np.float16))
+    for size, scale in ((1.0, 0.125), (1.0, 1e4), (100.0, 1e-4)):
+        q = queries(4, 4, D, seed=9, size=size)
+        say(f"[gpu] attend tiny and huge values size={size} scale={scale}")
+        got = c.attend(torch.from_numpy(q).cuda(), *b.args(), scale=scale)
+        # at 1e4 the scores of the last two sequences reach 1e8: fp32 sums are then off by whole units, so those two
+        # are held only where the scores are small enough
+        check_attend(b, enc, q, got, scale, f"scale {scale}", skip=(2, 3) if scale == 1e4 else ())
+        assert torch.isfinite(got).all().item()
+    # any finite scale: the largest score wins
+    q = queries(4, 4, D, seed=9)
+    got = c.attend(torch.from_numpy(q).cuda(), *b.args(), scale=1e37)
+    for s in (1, 3):
+        k, v = oc.values(enc[s][0]), oc.values(enc[s][1])
+        for h in range(4):
+            best = np.sort(k[:, h // 2] @ q[s, h].astype(np.float64))
+            if best[-1] - best[-2] > 1e-3 * best[-1]:
+                want = v[np.argmax(k[:, h // 2] @ q[s, h].astype(np.float64)), h // 2]
+                assert np.abs(got[s, h].float().cpu().numpy() - want).max() <= 2.0 ** -10 * np.abs(want).max() + 2.0 ** -24
 
 
 @pytest.mark.gpu
