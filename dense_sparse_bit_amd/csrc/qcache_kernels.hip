@@ -706,8 +706,6 @@ __device__ __forceinline__ void read_values(const uint8_t* tile, int lane, Value
 }
 
 // Scores of a tile: st[e][i] = token 4 kq + i of unit e against column n, in units of the column's k_l.
-// The scheduling barriers keep one group's operands in registers at a time: left to itself the compiler
-// unpacks all of them first, and the kernel spills.
 template <int D, int NG>
 __device__ __forceinline__ void tile_scores(const KeyRegs<D, NG> (&r)[2], const u32x4_t (&qf)[D / 32], u32x4_t qs,
                                             float (&st)[2][4]) {
@@ -737,7 +735,6 @@ __device__ __forceinline__ void tile_scores(const KeyRegs<D, NG> (&r)[2], const 
     if (g > 0) scale(g - 1);
     acc[0] = nxt[0];
     acc[1] = nxt[1];
-    __builtin_amdgcn_sched_barrier(0);
   }
   floatx4_t la[2];
 #pragma unroll
@@ -752,7 +749,6 @@ __device__ __forceinline__ void tile_scores(const KeyRegs<D, NG> (&r)[2], const 
   for (int e = 0; e < 2; ++e)
 #pragma unroll
     for (int i = 0; i < 4; ++i) st[e][i] = t[e][i] * 16777216.f + la[e][i];  // the codes were c 2^-24
-  __builtin_amdgcn_sched_barrier(0);
 }
 
 // Workgroups of a CU at once, by their registers.
@@ -1041,7 +1037,6 @@ k_qcache_attend(AttendArgs a) {
             av[x] = as_u32(q * as_h2(c[x / 2].vs[x & 1]) + as_h2(c[x / 2].vs[2 + (x & 1)]));
           }
           o[4 * cc + i] = mfma(av, pf, o[4 * cc + i]);
-          __builtin_amdgcn_sched_barrier(0);
         }
       }
     }
