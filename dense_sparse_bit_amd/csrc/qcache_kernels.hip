@@ -95,7 +95,6 @@ __device__ __forceinline__ uint32_t pk_h(float a, float b) {  // round to neares
 }
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }  // 1 ulp; results below 2^-126 are 0
 
-
 // x / d for 0 <= x < 2^31 as a multiplication: M = 2^(31 + sh) / d + 1, 2^(sh - 1) < d <= 2^sh.
 struct Divisor {
   uint32_t d, mul, sh;
@@ -117,7 +116,13 @@ inline Divisor divisor(int d) {
 // of the keys one token and D/32 runs of 8 dimensions, of the values D/16
 // dimensions of four tokens.  So a unit's codes are one contiguous 16 bytes
 // a lane (head_dim 128), and rows of FP16 or fp32 are read and written in runs
-// of 16 bytes or more.  Both kernels are bound by HBM.
+// of 16 bytes or more.
+//
+// Long calls are bound by HBM: 65536 tokens of 8 heads x 128 take 94 us to
+// write from FP16 (352 MB) and 125 us to read in fp32 (621 MB), 219 together
+// where a plain copy's rate allows 203.  Writing sits close to the VALU as well:
+// with fp32 divisions (22 instructions a value; some 11 now) it took 112 us.
+// A step of 16 tokens of 32 heads takes 3.4 us either way, a launch.
 //
 // Waves are numbered without knowing the lengths: sequence s owns the numbers
 // from (its first row / 16) + 2 s on, which leaves room for a unit at either end
@@ -523,13 +528,27 @@ k_qcache_read(const uint8_t* __restrict__ cache, Seqs sq, Rows k, Rows v, int he
 //   O = V^T p    rows = dimensions; p is already where the B operand wants it.
 //                Values are formed in FP16, lo + s q rounded once.
 //
+// The roundings to FP16 of p and of the values are each 2^-11 of a term at most
+// and independent, and what is left of them in an output is about its own
+// rounding (measured: 2-norm 3.3e-4 in all, 2.1e-4 of it the output's).  The rest
+// of p in a second MFMA brought 2.7e-4 and cost 3 to 8 % (16 x 8 heads x 32768:
+// 129 -> 140 us).
+//
 // q is scaled per row by a power of two so that its largest element is in
 // [64, 128): sums over a group stay in FP16's range, and q / 16 is exact down
 // to 2^-20 of the largest element.
 //
 // A wave's next 32 positions are copied from HBM straight into its own part of
-// LDS while it works on the current ones, which it holds in registers; the
-// units' statistics, which 4 or 16 lanes share, then cross HBM once.
+// LDS while it works on the current ones; the units' statistics, which 4 or 16
+// lanes share, then cross HBM once.  Registers would not do: two tiles of them
+// leave two waves a SIMD (63 against 51 us for 32 heads x 32768 positions), and
+// a second tile ahead in LDS (keys and values in rings of their own) costs more
+// copy instructions than it hides (128 -> 136 us for 16 x 8 heads x 32768).
+//
+// Long contexts are bound by what three workgroups a CU keep on its way from
+// HBM: 5.1 to 5.4 TB/s (a copy of the same card: 4.8; a plain read: 6.8) with the
+// VALU busy for half of the time.  Short ones are bound by the chain of loads
+// (lengths, pages, tile) of one workgroup: 8 us for 32 heads x 181 positions.
 //
 // At the end of an item's blocks the four waves' (m, sum, O) meet in LDS.  An
 // item that lies in one workgroup's range is finished there; otherwise each
@@ -565,6 +584,7 @@ struct AttendArgs {
 // Sequence s: its length, first row and rows, the blocks of an item, an item's cost and the items.  The cost is what
 // ranges are cut by: one per block and kItemCost for the item's start and end (its pages and q, the waves'
 // meeting), which come after the blocks; or 1, where ranges are cut between items only.
+// Ragged batches gain (31 sequences of 100 to 9000 positions: 55 us without the cost, 40 with), others are as they were.
 constexpr int kItemCost = 3;
 struct SeqWork {
   int len, first, n, nb, cost, items;
@@ -751,7 +771,9 @@ __device__ __forceinline__ void tile_scores(const KeyRegs<D, NG> (&r)[2], const 
     for (int i = 0; i < 4; ++i) st[e][i] = t[e][i] * 16777216.f + la[e][i];  // the codes were c 2^-24
 }
 
-// Workgroups of a CU at once, by their registers.
+// Workgroups of a CU at once, by their registers (with 4 of head_dim 128, groups of 32 spill: 51 -> 61 us for 32 heads
+// x 32768 positions, and with larger groups the additional partials cost more than they bring: 32 -> 36 us for sixteen
+// ragged sequences).
 constexpr int attend_resident(int D) { return D == 256 ? 2 : D == 128 ? 3 : 4; }
 
 template <int D, int NG>
