@@ -859,7 +859,10 @@ k_qcache_attend(AttendArgs a) {
       start += sw.cost * sw.items;
       item = blk = 0;
       do {
-        if (++s >= sq.n_seq) return;
+        if (++s >= sq.n_seq) {  // only if q_start or lens have changed meanwhile
+          if (threadIdx.x == 0) join[0] = -1;
+          return;
+        }
         const SeqWork x = seq_work(a, s);
         auto get = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
         sw = SeqWork{get(x.len), get(x.first), get(x.n), get(x.nb), get(x.cost), get(x.items)};
@@ -1126,7 +1129,7 @@ k_qcache_join(AttendArgs a) {
   __shared__ floatx4_t s_v[kJoinThreads];
   __shared__ float s_m[kJoinThreads], s_l[kJoinThreads];
   const int4 j = *(const int4*)(a.ws_join + 4 * blockIdx.x);
-  const int g = blockIdx.x, last = j.x, first = j.y, item = j.z, nrows = j.w;
+  const int g = blockIdx.x, last = min(j.x, a.grid - 1), first = j.y, item = j.z, nrows = j.w;
   if (last < 0) return;
   const int rt = a.by_heads.of(item), h = item - rt * a.heads;
   static_assert(16 * (256 / 4) <= 2 * kJoinThreads, "at most two passes");

@@ -26,6 +26,9 @@ import torch
 from .qgemv import QgemvError, _check, _launch, _stream_here, lib as _qgemv_lib
 
 
+_MAX = 2**31 - 1
+
+
 class Shape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("n_pages", "n_heads", "head_dim", "page_size", "group")]
 
@@ -63,6 +66,8 @@ def lib() -> ctypes.CDLL:
 
 def cache_bytes(n_pages, n_heads, head_dim, page_size=64, group=32) -> int:
     """Bytes of a cache of that shape."""
+    if max(n_pages, n_heads, head_dim, page_size, group) > _MAX:
+        raise ValueError("counts are 32-bit")
     n = ctypes.c_size_t(0)
     _check(lib().qcache_bytes(ctypes.byref(Shape(n_pages, n_heads, head_dim, page_size, group)), ctypes.byref(n)),
            "qcache_bytes")
@@ -91,6 +96,8 @@ class QCache:
         P = pages.shape[-1]
         if pages.dtype != i32 or pages.shape != (S, P) or not pages.is_contiguous() or pages.get_device() != at:
             raise ValueError("pages must be a contiguous int32 [S, P] tensor on the cache's device")
+        if S > _MAX or P > _MAX or n_tok > _MAX:
+            raise ValueError("counts are 32-bit")
         if q_start is None:
             if n_tok != S:
                 raise ValueError("without q_start there is one row per sequence")
@@ -100,7 +107,7 @@ class QCache:
             raise ValueError("q_start must be a contiguous int32 [S + 1] tensor on the cache's device")
         return Seqs(S, n_tok, P, q_start.data_ptr(), lens.data_ptr(), pages.data_ptr())
 
-    def _rows(self, t, heads, what, at):
+    def _rows(self, t, heads, what, at, written=False):
         """A [T, heads, head_dim] tensor as the library takes it; a stride that does not matter is 0."""
         dt, T = t.dtype, t.shape[0]
         if (dt != torch.float16 and dt != torch.float32) or t.shape != (T, heads, self.head_dim) or (
@@ -109,6 +116,13 @@ class QCache:
         ts, hs, one = t.stride()
         if one != 1:
             raise ValueError(f"{what}: the last dimension must be contiguous")
+        if written:
+            span = self.head_dim
+            for stride, n in sorted(((ts, T), (hs, heads))):
+                if n > 1 and stride < span:
+                    raise ValueError(f"{what}: vectors must not overlap")
+                if n > 1:
+                    span += stride * (n - 1)
         return Rows(t.data_ptr(), dt == torch.float32, ts if T > 1 else 0, hs if heads > 1 else 0)
 
     def write(self, k, v, lens, pages, q_start=None, stream=None):
@@ -155,7 +169,7 @@ class QCache:
             raise ValueError("give both k and v, or neither")
         elif dtype is not None and dtype != k.dtype:
             raise ValueError("dtype is not that of k and v")
-        kr, vr = self._rows(k, self.n_heads, "k", at), self._rows(v, self.n_heads, "v", at)
+        kr, vr = self._rows(k, self.n_heads, "k", at, True), self._rows(v, self.n_heads, "v", at, True)
         if v.shape[0] != k.shape[0] or kr.type != vr.type or n_tok not in (None, k.shape[0]):
             raise ValueError("k and v must have the same shape and type, and n_tok rows")
         sq = self._seqs(lens, pages, q_start, k.shape[0], at)
@@ -191,7 +205,7 @@ class QCache:
         else:
             if out.shape != q.shape or out.dtype != torch.float16:
                 raise ValueError("out must be FP16 in the shape of q")
-            orow = self._rows(out, H, "out", at)
+            orow = self._rows(out, H, "out", at, True)
         n = ctypes.c_size_t(0)
         L = lib()
         st = L.qcache_attend_ws(self._shape, sq, H, n)

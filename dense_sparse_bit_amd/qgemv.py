@@ -106,6 +106,8 @@ def lib() -> ctypes.CDLL:
 def _stream_here(index: int, stream):
     """The HIP stream to launch on where the device `index` is current and no stream is asked for, else None."""
     import torch
+    if index < 0:
+        raise ValueError("the memory must be on a GPU")
     if stream is None and torch._C._cuda_getDevice() == index:
         return torch._C._cuda_getCurrentRawStream(index)
     return None

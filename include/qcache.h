@@ -69,7 +69,8 @@ typedef struct {
  * Rows of vectors [n_tok][heads][head_dim] in device memory: the vector of row
  * t and head h starts at element t * tok_stride + h * head_stride.  type:
  * qgemv_dtype.  data is 16-byte aligned and both strides are multiples of 8
- * elements, so that vectors start on 16 bytes.
+ * elements, so that vectors start on 16 bytes.  Vectors that are written must
+ * not overlap; of those only read, a stride may be 0.
  */
 typedef struct {
   void* data;

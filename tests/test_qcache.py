@@ -326,6 +326,56 @@ def test_strided_views_and_refusals(torch):
     torch.cuda.synchronize()
 
 
+def test_memory_not_on_a_gpu():
+    torch = pytest.importorskip("torch")
+    c = qcache.QCache(2, 1, 64, page_size=16, device="cpu")
+    lens, pages = torch.ones(1, dtype=torch.int32), torch.zeros((1, 1), dtype=torch.int32)
+    x = torch.zeros((1, 1, 64), dtype=torch.float16)
+    for call in (lambda: c.write(x, x, lens, pages), lambda: c.read(lens, pages), lambda: c.attend(x, lens, pages)):
+        with pytest.raises(ValueError):
+            call()
+
+
+@pytest.mark.parametrize("i", range(5))
+def test_counts_past_32_bits(i):
+    shape = [1, 1, 64, 64, 32]
+    shape[i] += 2**32
+    with pytest.raises(ValueError):
+        qcache.cache_bytes(*shape)
+
+
+def test_written_vectors_must_not_overlap():
+    torch = pytest.importorskip("torch")
+    T, H, D = 3, 2, 64
+    c = qcache.QCache(1, H, D, device="cpu")
+    x = torch.zeros(T * H * D + 64)
+    wide = torch.zeros((T, H, 2 * D))
+    for good in (x[:T * H * D].view(T, H, D), x[:T * H * D].view(H, T, D).transpose(0, 1), wide[:, :, D:],
+                 x[:H * D].view(1, H, D), x[:0].view(0, H, D)):
+        c._rows(good, H, "out", -1, True)
+    for bad in (x[:H * D].view(1, H, D).expand(T, H, D), x[:T * D].view(T, 1, D).expand(T, H, D),
+                x.as_strided((T, H, D), (H * D - 8, D, 1)), x.as_strided((T, H, D), (D, T * D - 8, 1)),
+                x.as_strided((T, H, D), (D, D, 1)), x.as_strided((T, H, D), (H * D, D - 8, 1))):
+        c._rows(bad, H, "k", -1)  # fine to read from
+        with pytest.raises(ValueError):
+            c._rows(bad, H, "out", -1, True)
+
+
+@pytest.mark.gpu
+def test_outputs_that_overlap_refused(torch):
+    T, H, D = 5, 2, 64
+    b = Batch(torch, [T], [T], 32)
+    c = qcache.QCache(b.total, H, D, page_size=32)
+    k = torch.randn((1, H, D), device="cuda").half().expand(T, H, D)  # one vector for every row may be written from
+    c.write(k, k, *b.args())
+    kk, vv = c.read(*b.args(), n_tok=T)
+    assert np.array_equal(kk[3].cpu().numpy(), oc.held(k[:1].cpu().numpy(), 32).astype(np.float16)[0])
+    with pytest.raises(ValueError):
+        c.read(*b.args(), k=kk[:1].expand(T, H, D), v=vv)
+    with pytest.raises(ValueError):
+        c.attend(kk, *b.args(), out=vv[:1].expand(T, H, D))
+
+
 # ---- attention ----------------------------------------------------------------
 def fill(torch, b, H, D, G, seed, spread=1.0, keys=None, vals=None):
     """A cache holding every sequence of b whole; returns it and the held (encoded) keys and values."""
