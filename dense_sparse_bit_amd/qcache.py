@@ -164,15 +164,19 @@ class QCache:
                 dtype = torch.float16
             elif dtype != torch.float16 and dtype != torch.float32:
                 raise ValueError("dtype must be torch.float16 or torch.float32")
-            k, v = torch.empty((2, n_tok, self.n_heads, self.head_dim), dtype=dtype, device=self.data.device).unbind(0)
+            H, D = self.n_heads, self.head_dim
+            k, v = torch.empty((2, n_tok, H, D), dtype=dtype, device=self.data.device).unbind(0)
+            kr, vr = (Rows(t.data_ptr(), dtype == torch.float32, H * D, D) for t in (k, v))
         elif k is None or v is None:
             raise ValueError("give both k and v, or neither")
-        elif dtype is not None and dtype != k.dtype:
-            raise ValueError("dtype is not that of k and v")
-        kr, vr = self._rows(k, self.n_heads, "k", at, True), self._rows(v, self.n_heads, "v", at, True)
-        if v.shape[0] != k.shape[0] or kr.type != vr.type or n_tok not in (None, k.shape[0]):
-            raise ValueError("k and v must have the same shape and type, and n_tok rows")
-        sq = self._seqs(lens, pages, q_start, k.shape[0], at)
+        else:
+            kr, vr = self._rows(k, self.n_heads, "k", at, True), self._rows(v, self.n_heads, "v", at, True)
+            if v.shape[0] != k.shape[0] or kr.type != vr.type or n_tok not in (None, k.shape[0]):
+                raise ValueError("k and v must have the same shape and type, and n_tok rows")
+            if dtype is not None and dtype != k.dtype:
+                raise ValueError("dtype is not that of k and v")
+            n_tok = k.shape[0]
+        sq = self._seqs(lens, pages, q_start, n_tok, at)
         st = lib().qcache_read(self._shape, self.data.data_ptr(), sq, kr, vr, s)
         if st != 0:
             raise QgemvError(st, "qcache_read")
