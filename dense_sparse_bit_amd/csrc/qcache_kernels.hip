@@ -523,16 +523,16 @@ k_qcache_read(const uint8_t* __restrict__ cache, Seqs sq, Rows k, Rows v, int he
 //                instead.  Each group's sum is scaled by its step in fp32; the
 //                lowest values are one more MFMA, lo[token][group] times the
 //                sum of q over the group (as an FP16 part and its FP16 rest).
-//   p = exp2(S - m), with a running maximum m per column that is raised only
-//                when a score passes it by 8 (p stays below 2^8), and the sum.
-//   O = V^T p    rows = dimensions; p is already where the B operand wants it.
-//                Values are formed in FP16, lo + s q rounded once.
+//   p = exp2(S - m), with a reference m per column: 7 below the largest score
+//                when it was set, set anew only when a score passes it by 15.
+//                So p lies below 2^15, and FP16 holds what is 2^-31 of the largest.
+//   O = V^T p    rows = dimensions; p is already where the B operand wants it, as
+//                an FP16 part and its FP16 rest, each in an MFMA.  Values are
+//                formed in FP16, lo + s q rounded once.
 //
-// The roundings to FP16 of p and of the values are each 2^-11 of a term at most
-// and independent, and what is left of them in an output is about its own
-// rounding (measured: 2-norm 3.3e-4 in all, 2.1e-4 of it the output's).  The rest
-// of p in a second MFMA brought 2.7e-4 and cost 3 to 8 % (16 x 8 heads x 32768:
-// 129 -> 140 us).
+// Without the rest of p its rounding counts as much as the values' and the
+// output's do: 3.3e-4 of the outputs' 2-norm in all, 2.7e-4 with it, 2.1e-4 for
+// the output's alone.  It costs 1 to 5 % (16 x 8 heads x 32768: 128 -> 134 us).
 //
 // q is scaled per row by a power of two so that its largest element is in
 // [64, 128): sums over a group stay in FP16's range, and q / 16 is exact down
@@ -546,7 +546,7 @@ k_qcache_read(const uint8_t* __restrict__ cache, Seqs sq, Rows k, Rows v, int he
 // copy instructions than it hides (128 -> 136 us for 16 x 8 heads x 32768).
 //
 // Long contexts are bound by what three workgroups a CU keep on its way from
-// HBM: 5.1 to 5.4 TB/s (a copy of the same card: 4.8; a plain read: 6.8) with the
+// HBM: 5.0 to 5.4 TB/s (a copy of the same card: 4.8; a plain read: 6.8) with the
 // VALU busy for half of the time.  Short ones are bound by the chain of loads
 // (lengths, pages, tile) of one workgroup: 8 us for 32 heads x 181 positions.
 //
@@ -617,6 +617,13 @@ __device__ __forceinline__ int wave_scan(int v) {  // inclusive
 // kept in registers across a loop that has none to spare.
 __device__ __forceinline__ int opaque(int v) {
   asm volatile("" : "+v"(v));
+  return v;
+}
+
+// -1, unknown to the compiler: p - h as h * -1 + p is one instruction with h's conversion from FP16.
+__device__ __forceinline__ float minus_one() {
+  float v = -1.f;
+  asm("" : "+s"(v));
   return v;
 }
 
@@ -739,7 +746,7 @@ __device__ __forceinline__ void tile_scores(const KeyRegs<D, NG> (&r)[2], const 
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float step = h2f((uint16_t)(r[e].ks[2 * g + i / 2] >> (16 * (i & 1))));
-        t[e][i] = g == 0 ? step * acc[e][i] : step * acc[e][i] + t[e][i];
+        t[e][i] = __builtin_fmaf(step, acc[e][i], g == 0 ? 0.f : t[e][i]);  // + 0: one instruction, with the conversion
       }
   };
 #pragma unroll
@@ -923,7 +930,7 @@ k_qcache_attend(AttendArgs a) {
     // q: B operands, scaled by 2^e (and by 1/16 more where the code pair stays shifted).
     u32x4_t qf[L::ND];
     u32x4_t qs = {0u, 0u, 0u, 0u};
-    float k_l, raise;  // log2 units of a score; how far a score may pass m
+    float k_l, raise;  // log2 units of a score; 15 of them as scores, how far one may pass m
     {
       float top = 0.f;
 #pragma unroll
@@ -932,9 +939,9 @@ k_qcache_attend(AttendArgs a) {
         for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf((float)qv[j][i]));
       top = column_max(top);
       const int e = top > 0.f && top <= 65504.f ? 6 - ilogbf(top) : 0;
-      // never 0 nor infinite, and 8 / k_l finite: all meet infinities below
+      // never 0 nor infinite, and 15 / k_l finite: all meet infinities below
       k_l = fminf(fmaxf(ldexpf(fabsf(a.scale2), -e), 1e-37f), 1e30f);
-      raise = 8.f / k_l;
+      raise = 15.f / k_l;
       const float up = a.scale2 < 0.f ? -ldexpf(1.f, e) : ldexpf(1.f, e);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
@@ -961,8 +968,9 @@ k_qcache_attend(AttendArgs a) {
     floatx4_t o[DL];
 #pragma unroll
     for (int j = 0; j < DL; ++j) o[j] = (floatx4_t){0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, mu = 0.f, l = 0.f;  // m in units of k_l; m, but 0 while it is -inf; sum of p
+    float m = -INFINITY, mu = 0.f, l = 0.f;  // m as a score; m, but 0 while it is -inf; sum of p
 
+    const float minus = minus_one();
     for (int j = 0; j < nt; ++j) {
       const int base = 128 * (k0 + j) + 32 * w;
       const bool on0 = p0 >= 0, on1 = p1 >= 0;
@@ -989,8 +997,8 @@ k_qcache_attend(AttendArgs a) {
       float top = st[0][0];
 #pragma unroll
       for (int i = 1; i < 8; ++i) top = fmaxf(top, st[i / 4][i % 4]);
-      if (__ballot(top > m + raise)) {
-        const float mn = fmaxf(m, column_max(top));
+      if (__ballot(top - m > raise)) {  // the difference: m + raise could be rounded past what FP16 holds
+        const float mn = fmaxf(m, column_max(top) - raise * (7.f / 15.f));
         const float f = mn == m ? 1.f : exp2_(k_l * (m - mn));
         m = mn;
         mu = mn == -INFINITY ? 0.f : mn;
@@ -998,18 +1006,22 @@ k_qcache_attend(AttendArgs a) {
 #pragma unroll
         for (int j2 = 0; j2 < DL; ++j2) o[j2] *= f;
       }
-      u32x4_t pf;
+      u32x4_t pf, pr;  // p in FP16, and the rest of it
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float p[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          // the difference first: exact near the maximum, and 1 there, however large the scores are
+          // the difference first: exact near the maximum, however large the scores are
           p[i] = exp2_(k_l * (st[e][i] - mu));
           l += p[i];
         }
-        pf[2 * e] = pk_h(p[0], p[1]);
-        pf[2 * e + 1] = pk_h(p[2], p[3]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          pf[2 * e + i] = pk_h(p[2 * i], p[2 * i + 1]);
+          const half2_t y = as_h2(pf[2 * e + i]);
+          pr[2 * e + i] = pk_h(__builtin_fmaf((float)y[0], minus, p[2 * i]), __builtin_fmaf((float)y[1], minus, p[2 * i + 1]));
+        }
       }
       ValueRegs<D> c[2];
       read_values<D, NG>(here, lane, c);
@@ -1062,6 +1074,7 @@ k_qcache_attend(AttendArgs a) {
             av[x] = as_u32(q * as_h2(c[x / 2].vs[x & 1]) + as_h2(c[x / 2].vs[2 + (x & 1)]));
           }
           o[4 * cc + i] = mfma(av, pf, o[4 * cc + i]);
+          o[4 * cc + i] = mfma(av, pr, o[4 * cc + i]);
         }
       }
     }

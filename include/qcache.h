@@ -111,7 +111,7 @@ int qcache_attend_ws(const qcache_shape* shape, const qcache_seqs* seqs, int32_t
  * out[t][h] = sum_p softmax_p(scale q[t][h] . k[p][h / r]) v[p][h / r],  r = n_q_heads / n_heads,
  * over the positions p of row t's sequence up to row t's own.  A row with no
  * such position is 0.  q and out are FP16; scores, softmax statistics and sums
- * are fp32, the weights and the values that they multiply FP16.
+ * are fp32, the weights two FP16 (22 bits), the values that they multiply FP16.
  * n_q_heads: a multiple of n_heads, at most 65535.  scale: finite, also times log2 e.
  * ws: device memory, 256-byte aligned, of qcache_attend_ws bytes, contents
  * undefined before and after; calls that may overlap in time need one each.

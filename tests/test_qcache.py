@@ -546,6 +546,43 @@ def test_attend_tiny_and_huge_values(torch):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("L,at", [(40000, 17), (40000, 39990), (5000, 2500)])
+def test_attend_thin_tail(torch, L, at):
+    """One position far above many whose values are large: each weight is 2^-26.5 of the largest, together they
+    are most of the output.  A weight is held to half of FP16's least step, 2^-25, where the largest is 2^7 or
+    more: to 2^-32 of it."""
+    D, G = 64, 32
+    tail = 400000.0 / L
+
+    def keys(s, k):
+        k = k * 0
+        k[at, :, 0] = 1
+        return k.astype(np.float16)
+
+    def vals(s, v):
+        v = v * 0.02 + tail
+        v[at] = np.linspace(-0.01, 0.01, D)
+        return v.astype(np.float16)
+
+    b = Batch(torch, [L], [1], 64, seed=9, one_each=True)
+    c, enc = fill(torch, b, 1, D, G, seed=6, keys=keys, vals=vals)
+    q = np.zeros((1, 2, D), np.float16)
+    q[:, :, 0] = 1
+    scale = 26.5 * math.log(2)
+    say(f"[gpu] attend thin tail L={L} at={at}")
+    got = c.attend(torch.from_numpy(q).cuda(), *b.args(), scale=scale)
+    check_attend(b, enc, q, got, scale, "thin tail")
+    k, v = (oc.values(e) for e in enc[0])
+    want, mean = oc.attend(q.astype(np.float64), k, v, scale, b.positions(0), None)
+    # values 2^-11, scores 2^-18 of 26.5 ln 2 in the exponent, sums (L / 32 + 16) 2^-24, and the weights as above
+    rel = 2 * 2.0 ** -11 + 2 * 2.0 ** -18 * scale + (L / 32 + 16) * 2.0 ** -24
+    tol = rel * (mean + np.abs(want)) + L * 2.0 ** -32 * np.abs(v).max() + 2.0 ** -25
+    err = np.abs(got.float().cpu().numpy() - want)
+    assert float((np.abs(want - v[at, 0]) / tol).min()) > 20  # the tail's part, which is what is looked at
+    assert float((err / tol).max()) <= 1
+
+
+@pytest.mark.gpu
 def test_attend_nan_and_missing_pages(torch):
     """A NaN or infinite value counts exactly for the rows that see its token; pages that are no pages are
     masked; what lies behind a sequence's end (all bits set here) never shows."""
