@@ -118,9 +118,9 @@ inline Divisor divisor(int d) {
 // a lane (head_dim 128), and rows of FP16 or fp32 are read and written in runs
 // of 16 bytes or more.
 //
-// Long calls are bound by HBM: 65536 tokens of 8 heads x 128 take 94 us to
-// write from FP16 (352 MB) and 125 us to read in fp32 (621 MB), 219 together
-// where a plain copy's rate allows 203.  Writing sits close to the VALU as well:
+// Long calls are bound by HBM, at a copy's rate (4.8 TB/s) or above: 65536 tokens
+// of 8 heads x 128 take 72 us to write from FP16 (352 MB) and 60 us to read in
+// FP16 (352 MB), 129 us in fp32 (621 MB).  Writing sits close to the VALU as well:
 // with fp32 divisions (22 instructions a value; some 11 now) it took 112 us.
 // A step of 16 tokens of 32 heads takes 3.4 us either way, a launch.
 //
@@ -165,14 +165,15 @@ __device__ __forceinline__ UnitTask unit_task(const Seqs& sq, int idx) {
 }
 inline int unit_waves(const Seqs& sq) { return sq.q_start ? sq.n_tok / 16 + 2 * sq.n_seq : sq.n_seq; }
 
-// N consecutive elements (a multiple of 4) as FP16 pairs / from fp32.
+// N consecutive elements (a multiple of 4) as FP16 pairs.  Rows are read once, past the L2's own keeping (65536 tokens
+// written and read, the inputs from HBM: 241 -> 217 us).
 template <int N>
 __device__ __forceinline__ void load_pairs(const Rows& r, int64_t e, uint32_t* h) {
   if (r.f32) {
     const floatx4_t* p = (const floatx4_t*)((const float*)r.data + e);
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
-      const floatx4_t x = p[i];
+      const floatx4_t x = __builtin_nontemporal_load(p + i);
       h[2 * i] = pk_h(x[0], x[1]);
       h[2 * i + 1] = pk_h(x[2], x[3]);
     }
@@ -180,7 +181,7 @@ __device__ __forceinline__ void load_pairs(const Rows& r, int64_t e, uint32_t* h
     const u32x4_t* p = (const u32x4_t*)((const _Float16*)r.data + e);
 #pragma unroll
     for (int i = 0; i < N / 8; ++i) {
-      const u32x4_t x = p[i];
+      const u32x4_t x = __builtin_nontemporal_load(p + i);
 #pragma unroll
       for (int k = 0; k < 4; ++k) h[4 * i + k] = x[k];
     }
@@ -189,24 +190,37 @@ __device__ __forceinline__ void load_pairs(const Rows& r, int64_t e, uint32_t* h
     h[0] = x[0], h[1] = x[1];
   }
 }
-template <int N>
-__device__ __forceinline__ void store_values(const Rows& r, int64_t e, const float* v) {
-  if (r.f32) {
-    floatx4_t* p = (floatx4_t*)((float*)r.data + e);
+// Outputs are stored 16 bytes a lane, lanes side by side, so that 64 or more bytes of a row leave together: only then
+// may they pass the L2 by: 65536 tokens are read in 60 us instead of 84 in FP16, in 129 instead of 151 in fp32 (and in
+// 225 with gaps between the lanes).
+__device__ __forceinline__ void stream_out(char* to, u32x4_t x) { __builtin_nontemporal_store(x, (u32x4_t*)to); }
+
+// The lane's two quads 2 kq, 2 kq + 1 of the 8 that the lanes of a column hold become quads kq and 4 + kq.
+__device__ __forceinline__ void by_column(u32x4_t& x, u32x4_t& y) {
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) p[i] = (floatx4_t){v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
-  } else if constexpr (N % 8 == 0) {
-    u32x4_t* p = (u32x4_t*)((_Float16*)r.data + e);
-#pragma unroll
-    for (int i = 0; i < N / 8; ++i) {
-      u32x4_t x;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = pk_h(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
-      p[i] = x;
-    }
-  } else {
-    *(u32x2_t*)((_Float16*)r.data + e) = (u32x2_t){pk_h(v[0], v[1]), pk_h(v[2], v[3])};
+  for (int i = 0; i < 4; ++i) {
+    const auto a = __builtin_amdgcn_permlane16_swap(x[i], y[i], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(a[0], a[1], false, false);
+    x[i] = b[0], y[i] = b[1];
   }
+}
+
+// The lane's quads Q m .. + Q - 1 of the 16 Q that 16 neighbouring lanes hold are stored at `row`, by way of LDS.
+template <int Q>
+__device__ __forceinline__ void store_row(char* row, u32x4_t (&x)[Q], int lane, u32x4_t* lds, bool on) {
+  const int m = lane & 15;
+  if constexpr (Q > 1) {
+    u32x4_t* mine = lds + (lane >> 4) * (16 * Q);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int i = 0; i < Q; ++i) mine[Q * m + i] = x[i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int i = 0; i < Q; ++i) x[i] = mine[16 * i + m];
+  }
+  if (!on) return;
+#pragma unroll
+  for (int i = 0; i < Q; ++i) stream_out(row + 16 * (16 * i + m), x[i]);
 }
 
 // Minimum and maximum of FP16 pairs, written out: the compiler's own quieten their operands first, which doubles them.
@@ -447,6 +461,7 @@ template <int D, int NG>
 __global__ void __launch_bounds__(256)
 k_qcache_read(const uint8_t* __restrict__ cache, Seqs sq, Rows k, Rows v, int heads, Divisor by_heads) {
   using L = Geo<D, NG>;
+  __shared__ u32x4_t s_row[2][D > 64 ? 64 * (D / 64) : 1];  // a value wave's row pieces, of fp32
   const int pair = by_heads.of(blockIdx.x), h = blockIdx.x - pair * heads;
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -478,17 +493,31 @@ k_qcache_read(const uint8_t* __restrict__ cache, Seqs sq, Rows k, Rows v, int he
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int pos = 16 * x.u + 4 * kq + i, hs = 16 * (i & 1);
-      if (pos < x.p0 || pos >= x.p0 + x.n) continue;
+      const bool on = pos >= x.p0 && pos < x.p0 + x.n;
       const float s = h2f((uint16_t)(st[i / 2] >> hs)), lo = h2f((uint16_t)(st[2 + i / 2] >> hs));
       float o[DL];
 #pragma unroll
       for (int j = 0; j < DL; ++j) o[j] = lo + s * (float)((c[(i >> 1) * L::NC + j / 4] >> (hs + 4 * (j & 3))) & 15u);
-      store_values<DL>(v, (int64_t)(x.row + pos - x.p0) * v.ts + (int64_t)h * v.hs + DL * n, o);
+      const int64_t e = (int64_t)(x.row + pos - x.p0) * v.ts + (int64_t)h * v.hs;
+      if (v.f32) {
+        u32x4_t y[DL / 4];
+#pragma unroll
+        for (int j = 0; j < DL / 4; ++j)
+          y[j] = __builtin_bit_cast(u32x4_t, (floatx4_t){o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]});
+        store_row<DL / 4>(v.data + 4 * e, y, lane, s_row[w >> 1], on);
+      } else if constexpr (DL >= 8) {
+        u32x4_t y[DL / 8];
+#pragma unroll
+        for (int j = 0; j < DL / 2; ++j) y[j / 4][j & 3] = pk_h(o[2 * j], o[2 * j + 1]);
+        store_row<DL / 8>(v.data + 2 * e, y, lane, s_row[w >> 1], on);
+      } else if (on) {
+        __builtin_nontemporal_store((u32x2_t){pk_h(o[0], o[1]), pk_h(o[2], o[3])}, (u32x2_t*)(v.data + 2 * e + 8 * n));
+      }
     }
   } else {
     const int pos = 16 * x.u + n;
-    if (pos < x.p0 || pos >= x.p0 + x.n) return;
-    const int64_t e = (int64_t)(x.row + pos - x.p0) * k.ts + (int64_t)h * k.hs + 8 * kq;
+    const bool on = pos >= x.p0 && pos < x.p0 + x.n;
+    const int64_t e = (int64_t)(x.row + pos - x.p0) * k.ts + (int64_t)h * k.hs;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       float s = 0.f, lo = 0.f;
@@ -501,7 +530,19 @@ k_qcache_read(const uint8_t* __restrict__ cache, Seqs sq, Rows k, Rows v, int he
         float o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = lo + s * (float)((c[j] >> (16 * (i & 1) + 4 * (i / 2))) & 15u);
-        store_values<8>(k, e + 32 * j, o);
+        if (k.f32) {
+          u32x4_t y = __builtin_bit_cast(u32x4_t, (floatx4_t){o[0], o[1], o[2], o[3]});
+          u32x4_t z = __builtin_bit_cast(u32x4_t, (floatx4_t){o[4], o[5], o[6], o[7]});
+          by_column(y, z);
+          char* to = k.data + 4 * (e + 32 * j) + 16 * kq;
+          if (on) {
+            stream_out(to, y);
+            stream_out(to + 64, z);
+          }
+        } else if (on) {
+          stream_out(k.data + 2 * (e + 32 * j) + 16 * kq,
+                     (u32x4_t){pk_h(o[0], o[1]), pk_h(o[2], o[3]), pk_h(o[4], o[5]), pk_h(o[6], o[7])});
+        }
       }
     }
   }
