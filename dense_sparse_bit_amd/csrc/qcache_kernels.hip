@@ -119,8 +119,8 @@ inline Divisor divisor(int d) {
 // of 16 bytes or more.
 //
 // Long calls are bound by HBM, at a copy's rate (4.8 TB/s) or above: 65536 tokens
-// of 8 heads x 128 take 72 us to write from FP16 (352 MB) and 60 us to read in
-// FP16 (352 MB), 129 us in fp32 (621 MB).  Writing sits close to the VALU as well:
+// of 8 heads x 128 take 70 us to write from FP16 (352 MB), 119 us from fp32
+// (621 MB), and 52 and 96 us to read.  Writing sits close to the VALU as well:
 // with fp32 divisions (22 instructions a value; some 11 now) it took 112 us.
 // A step of 16 tokens of 32 heads takes 3.4 us either way, a launch.
 //
@@ -190,9 +190,9 @@ __device__ __forceinline__ void load_pairs(const Rows& r, int64_t e, uint32_t* h
     h[0] = x[0], h[1] = x[1];
   }
 }
-// Outputs are stored 16 bytes a lane, lanes side by side, so that 64 or more bytes of a row leave together: only then
-// may they pass the L2 by: 65536 tokens are read in 60 us instead of 84 in FP16, in 129 instead of 151 in fp32 (and in
-// 225 with gaps between the lanes).
+// Outputs are stored 16 bytes a lane, lanes side by side, so that 128 or more bytes of a row leave together: only then
+// may they pass the L2 by: 65536 tokens are read in 52 us instead of 84 in FP16, in 96 instead of 151 in fp32 (pieces of
+// 64 bytes: 60 and 130; of 16 bytes: 225 in fp32).
 __device__ __forceinline__ void stream_out(char* to, u32x4_t x) { __builtin_nontemporal_store(x, (u32x4_t*)to); }
 
 // The lane's two quads 2 kq, 2 kq + 1 of the 8 that the lanes of a column hold become quads kq and 4 + kq.
@@ -202,6 +202,18 @@ __device__ __forceinline__ void by_column(u32x4_t& x, u32x4_t& y) {
     const auto a = __builtin_amdgcn_permlane16_swap(x[i], y[i], false, false);
     const auto b = __builtin_amdgcn_permlane32_swap(a[0], a[1], false, false);
     x[i] = b[0], y[i] = b[1];
+  }
+}
+
+// Two neighbouring lanes hold y and z of a token each; then y of both is the first token's and z the second's, in the
+// even lane what was y and in the odd lane what was z.
+__device__ __forceinline__ void by_pair(u32x4_t& y, u32x4_t& z, bool odd) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t mine = odd ? y[i] : z[i];
+    const uint32_t other = (uint32_t)__builtin_amdgcn_update_dpp((int)mine, (int)mine, 0xB1, 0xF, 0xF, false);  // i ^ 1
+    if (odd) y[i] = other;
+    else z[i] = other;
   }
 }
 
@@ -515,34 +527,48 @@ k_qcache_read(const uint8_t* __restrict__ cache, Seqs sq, Rows k, Rows v, int he
       }
     }
   } else {
-    const int pos = 16 * x.u + n;
-    const bool on = pos >= x.p0 && pos < x.p0 + x.n;
-    const int64_t e = (int64_t)(x.row + pos - x.p0) * k.ts + (int64_t)h * k.hs;
+    float s[NG], lo[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      float s = 0.f, lo = 0.f;
+      s[g] = lo[g] = 0.f;
       if (p >= 0) {
-        s = h2f(((const uint16_t*)(unit + L::off_ks))[((n >> 2) * NG + g) * 4 + (n & 3)]);
-        lo = h2f(((const uint16_t*)(unit + L::off_kl))[n * NG + g]);
+        s[g] = h2f(((const uint16_t*)(unit + L::off_ks))[((n >> 2) * NG + g) * 4 + (n & 3)]);
+        lo[g] = h2f(((const uint16_t*)(unit + L::off_kl))[n * NG + g]);
       }
+    }
+    // the rows of the lane's token pair; lane n even has the first half of each of its 128-byte pieces, n odd the second
+    const int pos = 16 * x.u + (n & ~1);
+    const bool on0 = pos >= x.p0 && pos < x.p0 + x.n, on1 = pos + 1 >= x.p0 && pos + 1 < x.p0 + x.n;
+    const int64_t el = k.f32 ? 4 : 2;
+    char* row0 = k.data + el * ((int64_t)(x.row + pos - x.p0) * k.ts + (int64_t)h * k.hs) + 64 * (n & 1) + 16 * kq;
+    char* row1 = row0 + el * k.ts;
+    auto put = [&](int at, u32x4_t y, u32x4_t z) {
+      by_pair(y, z, n & 1);
+      if (on0) stream_out(row0 + at, y);
+      if (on1) stream_out(row1 + at, z);
+    };
 #pragma unroll
-      for (int j = g * (L::G / 32); j < (g + 1) * (L::G / 32); ++j) {
-        float o[8];
+    for (int j2 = 0; j2 < L::ND; j2 += 2) {
+      float o[2][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = lo + s * (float)((c[j] >> (16 * (i & 1) + 4 * (i / 2))) & 15u);
-        if (k.f32) {
-          u32x4_t y = __builtin_bit_cast(u32x4_t, (floatx4_t){o[0], o[1], o[2], o[3]});
-          u32x4_t z = __builtin_bit_cast(u32x4_t, (floatx4_t){o[4], o[5], o[6], o[7]});
+      for (int r = 0; r < 2; ++r) {
+        const int g = 32 * (j2 + r) / L::G;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[r][i] = lo[g] + s[g] * (float)((c[j2 + r] >> (16 * (i & 1) + 4 * (i / 2))) & 15u);
+      }
+      if (k.f32) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          u32x4_t y = __builtin_bit_cast(u32x4_t, (floatx4_t){o[r][0], o[r][1], o[r][2], o[r][3]});
+          u32x4_t z = __builtin_bit_cast(u32x4_t, (floatx4_t){o[r][4], o[r][5], o[r][6], o[r][7]});
           by_column(y, z);
-          char* to = k.data + 4 * (e + 32 * j) + 16 * kq;
-          if (on) {
-            stream_out(to, y);
-            stream_out(to + 64, z);
-          }
-        } else if (on) {
-          stream_out(k.data + 2 * (e + 32 * j) + 16 * kq,
-                     (u32x4_t){pk_h(o[0], o[1]), pk_h(o[2], o[3]), pk_h(o[4], o[5]), pk_h(o[6], o[7])});
+          put(128 * (j2 + r), y, z);
         }
+      } else {
+        u32x4_t y, z;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = pk_h(o[0][2 * i], o[0][2 * i + 1]), z[i] = pk_h(o[1][2 * i], o[1][2 * i + 1]);
+        put(64 * j2, y, z);
       }
     }
   }
