@@ -614,7 +614,7 @@ k_qcache_read(const uint8_t* __restrict__ cache, Seqs sq, Rows k, Rows v, int he
 //
 // Long contexts are bound by what three workgroups a CU keep on its way from
 // HBM: 5.0 to 5.4 TB/s (a copy of the same card: 4.8; a plain read: 6.8) with the
-// VALU busy for half of the time.  Short ones are bound by the chain of loads
+// VALU busy for 70 % of the CUs' cycles.  Short ones are bound by the chain of loads
 // (lengths, pages, tile) of one workgroup: 8 us for 32 heads x 181 positions.
 //
 // At the end of an item's blocks the four waves' (m, sum, O) meet in LDS.  An
