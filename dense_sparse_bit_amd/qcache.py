@@ -165,7 +165,7 @@ class QCache:
             elif dtype != torch.float16 and dtype != torch.float32:
                 raise ValueError("dtype must be torch.float16 or torch.float32")
             H, D = self.n_heads, self.head_dim
-            k, v = torch.empty((2, n_tok, H, D), dtype=dtype, device=self.data.device).unbind(0)
+            k, v = self.data.new_empty(2, n_tok, H, D, dtype=dtype).unbind(0)
             kr, vr = (Rows(t.data_ptr(), dtype == torch.float32, H * D, D) for t in (k, v))
         elif k is None or v is None:
             raise ValueError("give both k and v, or neither")
@@ -204,7 +204,7 @@ class QCache:
         elif not math.isfinite(scale):
             raise ValueError("scale must be finite")
         if out is None:
-            out = torch.empty((T, H, self.head_dim), dtype=torch.float16, device=self.data.device)
+            out = q.new_empty(T, H, self.head_dim)
             orow = Rows(out.data_ptr(), 0, H * self.head_dim, self.head_dim)
         else:
             if out.shape != q.shape or out.dtype != torch.float16:
@@ -215,7 +215,7 @@ class QCache:
         st = L.qcache_attend_ws(self._shape, sq, H, n)
         if st == 0:
             # its own for every call: calls on other streams, and captured ones, never share it
-            ws = torch.empty(n.value, dtype=torch.uint8, device=self.data.device)
+            ws = self.data.new_empty(n.value)
             st = L.qcache_attend(self._shape, self.data.data_ptr(), sq, H, qr, orow, scale, ws.data_ptr(), n.value, s)
         if st != 0:
             raise QgemvError(st, "qcache_attend")

@@ -328,7 +328,7 @@ class QGemv:
                 dtype = f16
             elif dtype != f16 and dtype != f32:
                 raise ValueError("dtype must be torch.float16 or torch.float32")
-            out = torch.empty((B, mo), dtype=dtype, device=self.blob.device)
+            out = x.new_empty(B, mo, dtype=dtype)
             y, e.y_type = out.data_ptr(), dtype == f32
         else:
             if dtype is not None and dtype != out.dtype:
