@@ -639,6 +639,50 @@ def test_attend_table_shorter_than_the_lengths(torch):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("seed", range(24))
+def test_random_calls(torch, seed):
+    """Shapes, ragged and empty sequences, rows per sequence, padding, tables with holes, scales and output
+    strides drawn together; attention twice (the same bits), and the cache read back in both types."""
+    rng = np.random.default_rng(seed)
+    D, G = DIMS[seed % len(DIMS)]
+    H, per = int(rng.choice([1, 2, 3, 5])), int(rng.choice([1, 2, 3, 4, 7, 8, 17, 33]))
+    page, S = int(rng.choice([16, 32, 64, 128, 1024])), int(rng.choice([1, 2, 3, 5, 9, 20]))
+    top = int(np.exp(rng.uniform(0, math.log(5000 if S < 4 else 900))))
+    lens = [int(rng.integers(0, top + 1)) if rng.random() < 0.9 else 0 for _ in range(S)]
+    one_each = rng.random() < 0.4
+    new = [1] * S if one_each else [int(rng.choice([0, 1, 1, 2, 3, 7, 17])) for _ in range(S)]
+    b = Batch(torch, lens, new, page, pad=0 if one_each else int(rng.integers(1, 4)), seed=seed, one_each=one_each)
+    c, enc = fill(torch, b, H, D, G, seed=seed, spread=float(rng.choice([0.2, 1, 3])))
+    for _ in range(int(rng.integers(0, 5))):
+        b.table[rng.integers(S), rng.integers(b.table.shape[1])] = [-1, b.total, 1 << 29][rng.integers(3)]
+    b.d_pages.copy_(torch.from_numpy(b.table))
+    scale = float(rng.choice([1 / math.sqrt(D), 1.0, 0.01, -0.1]))
+    q = queries(b.n_tok, H * per, D, seed, float(rng.choice([1e-3, 0.3, 1, 4])))
+    say(f"[gpu] random call {seed}: D={D} G={G} H={H} per={per} page={page} S={S} lens<={top} rows={b.n_tok}")
+    end = int(b.start[-1])
+    out = torch.full((b.n_tok, H * per, D + 8), 7.0, device="cuda").half()
+    got = c.attend(torch.from_numpy(q).cuda(), *b.args(), scale=scale, out=out[:, :, :D])
+    check_attend(b, enc, q, got, scale, f"random call {seed}")
+    assert bool((out[:, :, D:] == 7).all()) and bool((out[end:] == 7).all())
+    again = c.attend(torch.from_numpy(q).cuda(), *b.args(), scale=scale)
+    assert torch.equal(again[:end], got[:end])
+    for dtype in (torch.float16, torch.float32):
+        wide = [torch.full((b.n_tok, H, D + 8), 3.0, device="cuda", dtype=dtype) for _ in range(2)]
+        c.read(*b.args(), k=wide[0][:, :, :D], v=wide[1][:, :, :D])
+        for i, w in enumerate(wide):
+            assert bool((w[:, :, D:] == 3).all()) and bool((w[end:] == 3).all())
+            for s in range(S):
+                pos = b.positions(s)
+                on = b.on_page(s, pos)
+                want = np.zeros((len(pos), H, D))
+                if on.any():
+                    want[on] = oc.values(enc[s][i])[pos[on]]
+                want = want.astype(np.float32)  # lo + s q in fp32, then the rows' type
+                g = w[b.start[s]:b.start[s + 1], :, :D].cpu().numpy()
+                assert np.array_equal(g, want if dtype == torch.float32 else want.astype(np.float16))
+
+
+@pytest.mark.gpu
 def test_attend_strided_q_and_out(torch):
     b = Batch(torch, [50, 333], [1, 1], 32, seed=1, one_each=True)
     c, enc = fill(torch, b, 2, 128, 64, seed=2)
