@@ -163,7 +163,12 @@ __device__ __forceinline__ UnitTask unit_task(const Seqs& sq, int idx) {
   x.s = lo;
   return x;
 }
-inline int unit_waves(const Seqs& sq) { return sq.q_start ? sq.n_tok / 16 + 2 * sq.n_seq : sq.n_seq; }
+// Workgroups of two units each.  T: Seqs or qcache_seqs.
+template <class T>
+inline int64_t unit_workgroups(const T& sq, int heads) {
+  const int64_t waves = sq.q_start ? (int64_t)sq.n_tok / 16 + 2 * (int64_t)sq.n_seq : sq.n_seq;
+  return (waves + 1) / 2 * heads;
+}
 
 // N consecutive elements (a multiple of 4) as FP16 pairs.  Rows are read once, past the L2's own keeping (65536 tokens
 // written and read, the inputs from HBM: 241 -> 217 us).
@@ -1325,14 +1330,14 @@ hipError_t by_shape(const qcache_shape* sh, F f) {
 template <int D, int NG>
 hipError_t launch_write(Dims<D, NG>, uint8_t* cache, const Seqs& sq, const Rows& k, const Rows& v, int heads,
                         hipStream_t st) {
-  hipLaunchKernelGGL((k_qcache_write<D, NG>), dim3((unit_waves(sq) + 1) / 2 * heads), dim3(256), 0, st, cache, sq, k, v,
+  hipLaunchKernelGGL((k_qcache_write<D, NG>), dim3((uint32_t)unit_workgroups(sq, heads)), dim3(256), 0, st, cache, sq, k, v,
                      heads, divisor(heads));
   return hipGetLastError();
 }
 template <int D, int NG>
 hipError_t launch_read(Dims<D, NG>, const uint8_t* cache, const Seqs& sq, const Rows& k, const Rows& v, int heads,
                        hipStream_t st) {
-  hipLaunchKernelGGL((k_qcache_read<D, NG>), dim3((unit_waves(sq) + 1) / 2 * heads), dim3(256), 0, st, cache, sq, k, v,
+  hipLaunchKernelGGL((k_qcache_read<D, NG>), dim3((uint32_t)unit_workgroups(sq, heads)), dim3(256), 0, st, cache, sq, k, v,
                      heads, divisor(heads));
   return hipGetLastError();
 }
@@ -1402,8 +1407,8 @@ static int check_copy(const qcache_shape* shape, const void* cache, const qcache
   if (seqs->n_seq == 0 || seqs->n_tok == 0) return QGEMV_OK;
   if ((st = check_rows(k)) || (st = check_rows(v))) return st;
   if (k->type != v->type) return QGEMV_ERR_INVALID_ARG;
-  // workgroups of a launch
-  if (((int64_t)seqs->n_tok / 32 + seqs->n_seq + 1) * shape->n_heads > 0x7FFFFFFF) return QGEMV_ERR_UNSUPPORTED;
+  // a grid holds fewer than 2^32 threads
+  if (unit_workgroups(*seqs, shape->n_heads) * 256 > 0xFFFFFFFFll) return QGEMV_ERR_UNSUPPORTED;
   return QGEMV_OK;
 }
 

@@ -88,7 +88,10 @@ int qcache_bytes(const qcache_shape* shape, size_t* bytes);
  * writes) leave either row's values or a mixture there.
  * Errors: INVALID_ARG (null pointer, misalignment, a negative count, n_tok
  * other than n_seq without q_start, k and v of different types), UNSUPPORTED
- * (shape, type), HIP.  n_seq or n_tok 0: nothing is done.
+ * (shape, type; n_seq above 2^28; max_pages * page_size above 2^31 - 1025;
+ * ceil(u / 2) * n_heads at 2^24, the workgroups of a launch, or more, with u =
+ * n_seq, or n_tok / 16 + 2 n_seq with q_start), HIP.  n_seq or n_tok 0: nothing
+ * is done.
  */
 int qcache_write(const qcache_shape* shape, void* cache, const qcache_seqs* seqs, const qcache_rows* k,
                  const qcache_rows* v, void* stream);
