@@ -607,8 +607,9 @@ k_qcache_read(const uint8_t* __restrict__ cache, Seqs sq, Rows k, Rows v, int he
 // the output's alone.  It costs 1 to 5 % (16 x 8 heads x 32768: 128 -> 134 us).
 //
 // q is scaled per row by a power of two so that its largest element is in
-// [64, 128): sums over a group stay in FP16's range, and q / 16 is exact down
-// to 2^-20 of the largest element.
+// [64, 128): sums over a group stay in FP16's range.  Elements are exact down to
+// 2^-20 of the largest, those divided by 16 down to 2^-16 of it; what is smaller
+// is rounded by at most 2^-31 and 2^-27 of the largest.
 //
 // A wave's next 32 positions are copied from HBM straight into its own part of
 // LDS while it works on the current ones; the units' statistics, which 4 or 16
@@ -618,8 +619,11 @@ k_qcache_read(const uint8_t* __restrict__ cache, Seqs sq, Rows k, Rows v, int he
 // copy instructions than it hides (128 -> 136 us for 16 x 8 heads x 32768).
 //
 // Long contexts are bound by what three workgroups a CU keep on its way from
-// HBM: 5.0 to 5.4 TB/s (a copy of the same card: 4.8; a plain read: 6.8) with the
-// VALU busy for 70 % of the CUs' cycles.  Short ones are bound by the chain of loads
+// HBM: 4.9 TB/s (168 MB, 34 us without the join) to 5.7 (672 MB, 119 us; a copy of the same
+// card: 4.8, a plain read: 6.8) with the VALU busy for 68 to 73 % of the CUs' cycles.
+// The loop's counters and addresses are scalars, more than fit: the compiler keeps
+// 72 to 83 of them in lanes of vector registers, and starting a tile's copy reads
+// some ten of them back.  Short contexts are bound by the chain of loads
 // (lengths, pages, tile) of one workgroup: 8 us for 32 heads x 181 positions.
 //
 // At the end of an item's blocks the four waves' (m, sum, O) meet in LDS.  An
@@ -891,7 +895,8 @@ k_qcache_attend(AttendArgs a) {
     return SeqWork{get(mine.len), get(mine.first), get(mine.n), get(mine.nb), get(mine.cost), get(mine.items)};
   };
 
-  // All blocks; rows of empty sequences become 0 on the way.
+  // All blocks; rows of empty sequences become 0 on the way.  Every workgroup looks at every sequence, 64 a round: 16
+  // sequences of 8192 positions take 40 us, among 128 in all 41, among 512 51, among 4096 159.
   int total = 0;
   for (int s0 = 0; s0 < sq.n_seq; s0 += 64) {
     load_chunk(s0);

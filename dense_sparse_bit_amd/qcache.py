@@ -148,7 +148,7 @@ class QCache:
         """(k, v): the values held where write() would have put the rows, [n_tok, n_heads, head_dim].
 
         Allocated as dtype (FP16 by default) if k and v are not given; rows of padding are then not
-        initialised.  n_tok: rows of the outputs, by default those of k, or one per sequence.
+        initialised.  k and v, if given, must not overlap each other.  n_tok: rows of the outputs, by default those of k, or one per sequence.
         """
         at = self.data.get_device()
         s = _stream_here(at, stream)

@@ -294,7 +294,8 @@ class QGemv:
 
         x: FP16 [B, K], contiguous, B in {1, 8, 16}.  bias [M] and residual [B, M or M // 2]: FP16 or fp32.
         act: "none", "relu", "gelu", "gelu_tanh" or "silu".  out: FP16 or fp32, allocated as dtype (FP16 by
-        default) if not given; out and residual may be rows of wider arrays, and residual may be out itself.
+        default) if not given; out and residual may be rows of wider arrays, and residual may be out itself; out
+        overlaps nothing else that the call reads.
         All on the plan's device; stream: as run().  With uniform codes at B 8 or 16 runs of one plan share its
         workspace and must not overlap, and the first must not be captured into a graph.
         """
