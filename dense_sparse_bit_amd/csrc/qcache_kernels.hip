@@ -619,8 +619,8 @@ k_qcache_read(const uint8_t* __restrict__ cache, Seqs sq, Rows k, Rows v, int he
 // copy instructions than it hides (128 -> 136 us for 16 x 8 heads x 32768).
 //
 // Long contexts are bound by what three workgroups a CU keep on its way from
-// HBM: 4.9 TB/s (168 MB, 34 us without the join) to 5.7 (672 MB, 119 us; a copy of the same
-// card: 4.8, a plain read: 6.8) with the VALU busy for 68 to 73 % of the CUs' cycles.
+// HBM: 4.9 TB/s (168 MB, 34 us without the join), 5.3 to 5.7 (672 MB, 119 to 127 us; a copy of
+// the same card: 4.8, a plain read: 6.8) with the VALU busy for 68 to 73 % of the CUs' cycles.
 // The loop's counters and addresses are scalars, more than fit: the compiler keeps
 // 72 to 83 of them in lanes of vector registers, and starting a tile's copy reads
 // some ten of them back.  Short contexts are bound by the chain of loads
