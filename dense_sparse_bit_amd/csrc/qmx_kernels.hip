@@ -1,0 +1,422 @@
+// qmx_kernels.hip -- rows in MX blocks: quantising, values, plain arrays, and
+// the product of two sets of blocks on the scaled MFMAs (include/qmx.h; storage
+// in qmx_layout.h).
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "../../include/qmx.h"
+#include "qgemv_epilogue_dev.h"
+#include "qgemv_internal.h"
+#include "qmx_blocks.h"
+#include "qmx_layout.h"
+
+using namespace qmx_layout;
+using namespace qmx_dev;
+
+namespace {
+
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+typedef float floatx4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+
+// ---------------------------------------------------------------------------
+// Quantising, and the values back.
+//
+// A wave takes a chunk (16 rows x 128 columns).  In each of four steps 16 lanes
+// take the 128 columns of a row, 8 columns a lane: rows move in contiguous 256
+// (FP16) or 512 (fp32) bytes, four neighbouring lanes hold a block, and its
+// largest value is two lane exchanges away.
+// ---------------------------------------------------------------------------
+template <bool F32>
+__device__ __forceinline__ void load8(const void* x, int64_t e, float (&v)[8]) {
+  if constexpr (F32) {
+    const floatx4_t* p = (const floatx4_t*)((const float*)x + e);
+    const floatx4_t a = __builtin_nontemporal_load(p), b = __builtin_nontemporal_load(p + 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+  } else {
+    const half8_t a = __builtin_bit_cast(half8_t, __builtin_nontemporal_load((const u32x4_t*)((const _Float16*)x + e)));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (float)a[i];
+  }
+}
+
+// Byte offset of the lane's elements of row r (of 16), columns 8 c .. + 7 of the chunk.
+template <int FMT>
+__device__ __forceinline__ int lane_bytes(int r, int c) {
+  return FMT == kE2M1 ? 16 * (16 * (c >> 2) + r) + 4 * (c & 3) : 1024 * (c >> 3) + 16 * (16 * ((c >> 1) & 3) + r) + 8 * (c & 1);
+}
+
+template <int FMT, bool F32>
+__global__ void __launch_bounds__(256)
+k_mx_quantize(uint8_t* __restrict__ blocks, Geo g, const void* __restrict__ x, int64_t ldx, int clip, int total) {
+  const int lane = threadIdx.x & 63;
+  const int id = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (id >= total) return;
+  const int tile = id / g.chunks, chunk = id - tile * g.chunks;
+  const int c = lane & 15, col = 128 * chunk + 8 * c;
+  uint8_t* to = blocks + tile * g.tile_bytes + (int64_t)chunk * (FMT ? 2048 : 1024);
+  uint8_t* ex = blocks + g.exps + ((int64_t)tile * g.quads + (chunk >> 2)) * 256 + (chunk & 3);
+  float v[4][8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 16 * tile + 4 * i + (lane >> 4);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
+    if (row < g.rows && col < g.cols) load8<F32>(x, row * ldx + col, v[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * i + (lane >> 4);
+    uint32_t w[2];
+    const uint32_t byte = mx_quad<FMT>(v[i], clip, w);
+    if (16 * tile + r >= g.rows) continue;
+    if constexpr (FMT == kE2M1) *(uint32_t*)(to + lane_bytes<FMT>(r, c)) = w[0];
+    else *(u32x2_t*)(to + lane_bytes<FMT>(r, c)) = (u32x2_t){w[0], w[1]};
+    if ((c & 3) == 0) ex[4 * (16 * (c >> 2) + r)] = (uint8_t)byte;
+  }
+}
+
+// The 8 values of E2M1 codes (a dword) or E4M3 codes (two).
+template <int FMT>
+__device__ __forceinline__ void decode8(const uint32_t* w, float step, float (&v)[8]) {
+  if constexpr (FMT == kE2M1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t q = w[0] >> (4 * i), m = q & 7;
+      // E2M1's bits in place of the top of an fp32's, times 2^126; 0.5 is the only subnormal
+      const float a = m < 2 ? 0.5f * (float)m : __uint_as_float((m << 22) + (126u << 23));
+      v[i] = (q & 8 ? -a : a) * step;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t q = w[i / 4] >> (8 * (i & 3)), m = q & 127;
+      const float a = m < 8 ? (float)m * 0.001953125f : m == 127 ? __uint_as_float(0x7FC00000u)
+                                                                 : __uint_as_float((m << 20) + (120u << 23));
+      v[i] = (q & 128 ? -a : a) * step;
+    }
+  }
+}
+
+template <int FMT, bool F32>
+__global__ void __launch_bounds__(256)
+k_mx_values(const uint8_t* __restrict__ blocks, Geo g, void* __restrict__ x, int64_t ldx, int total) {
+  const int lane = threadIdx.x & 63;
+  const int id = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (id >= total) return;
+  const int tile = id / g.chunks, chunk = id - tile * g.chunks;
+  const int c = lane & 15, col = 128 * chunk + 8 * c;
+  const uint8_t* from = blocks + tile * g.tile_bytes + (int64_t)chunk * (FMT ? 2048 : 1024);
+  const uint8_t* ex = blocks + g.exps + ((int64_t)tile * g.quads + (chunk >> 2)) * 256 + (chunk & 3);
+  if (col >= g.cols) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 4 * i + (lane >> 4), row = 16 * tile + r;
+    if (row >= g.rows) return;
+    uint32_t w[2];
+    w[0] = *(const uint32_t*)(from + lane_bytes<FMT>(r, c));
+    if constexpr (FMT == kE4M3) w[1] = *(const uint32_t*)(from + lane_bytes<FMT>(r, c) + 4);
+    float v[8];
+    decode8<FMT>(w, mx_step(ex[4 * (16 * (c >> 2) + r)]), v);
+    const int64_t e = row * ldx + col;
+    if constexpr (F32) {
+      floatx4_t* p = (floatx4_t*)((float*)x + e);
+      __builtin_nontemporal_store((floatx4_t){v[0], v[1], v[2], v[3]}, p);
+      __builtin_nontemporal_store((floatx4_t){v[4], v[5], v[6], v[7]}, p + 1);
+    } else {
+      half8_t h;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[k] = (_Float16)v[k];
+      __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, h), (u32x4_t*)((_Float16*)x + e));
+    }
+  }
+}
+
+// A lane moves one block: 16 or 32 bytes and its exponent byte.
+template <int FMT, bool PACK>
+__global__ void __launch_bounds__(256)
+k_mx_plain(uint8_t* __restrict__ blocks, Geo g, uint8_t* __restrict__ codes, uint8_t* __restrict__ exps, int total) {
+  constexpr int parts = FMT ? 2 : 1;
+  const int lane = threadIdx.x & 63;
+  const int id = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (id >= total) return;
+  const int tile = id / g.chunks, chunk = id - tile * g.chunks;
+  const int row = 16 * tile + (lane & 15), b = 4 * chunk + (lane >> 4), nb = g.cols / 32;
+  const bool real = row < g.rows && b < nb;
+  uint8_t* at = blocks + tile * g.tile_bytes + (int64_t)chunk * (1024 * parts);
+  uint8_t* ex = blocks + g.exps + ((int64_t)tile * g.quads + (chunk >> 2)) * 256 + 4 * lane + (chunk & 3);
+  if (!PACK && !real) return;
+  const int64_t plain = ((int64_t)row * nb + b);
+#pragma unroll
+  for (int p = 0; p < parts; ++p) {
+    u32x4_t* in = (u32x4_t*)(codes + plain * (16 * parts) + 16 * p);
+    u32x4_t* bl = (u32x4_t*)(at + lane_bytes<FMT>(lane & 15, 4 * (lane >> 4) + 2 * p));
+    if constexpr (PACK) *bl = real ? *in : (u32x4_t){0, 0, 0, 0};
+    else *in = *bl;
+  }
+  if constexpr (PACK) *ex = real ? exps[plain] : 1;
+  else exps[plain] = *ex;
+}
+
+// ---------------------------------------------------------------------------
+// The product.  Weights are the A operand (16 features), activation rows the B
+// operand (16 tokens): lane 16 q + n of a result holds features 4 q .. + 3 of
+// token n, so a lane's outputs are neighbours in memory and a gated pair is in one
+// lane.
+// ---------------------------------------------------------------------------
+struct Side {
+  const uint8_t* codes;
+  const uint8_t* exps;
+  int64_t tile_bytes;
+  int tiles;
+};
+
+__device__ __forceinline__ i32x8_t operand(const uint8_t* p, int lane, bool two) {
+  const u32x4_t a = *(const u32x4_t*)(p + 16 * lane);
+  u32x4_t b = {0, 0, 0, 0};
+  if (two) b = *(const u32x4_t*)(p + 1024 + 16 * lane);
+  return (i32x8_t){(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+}
+
+template <int FMT, int J>
+__device__ __forceinline__ floatx4_t mx_mfma(i32x8_t a, i32x8_t b, floatx4_t c, int ea, int eb) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, FMT == kE2M1 ? 4 : 0, J, ea, J, eb);
+}
+
+// The lane's four features of one token.
+__device__ __forceinline__ void put4(const EpiArg<true>& ep, int M, int T, int row, int t, floatx4_t s) {
+  if (t >= T) return;
+  if (ep.gated) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2)
+      if (row + i < M) ep.put_gated(t, row + i, s[i], s[i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (row + i < M) ep.put(t, row + i, s[i]);
+  }
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(256)
+k_mx_simple(Side w, Side x, EpiArg<true> ep, int M, int T, int chunks, int quads) {
+  constexpr int AT = 2, BT = 2;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int a0 = (blockIdx.x * 4 + wave) * AT, b0 = blockIdx.y * BT;
+  if (a0 >= w.tiles) return;
+  floatx4_t acc[AT][BT];
+#pragma unroll
+  for (int i = 0; i < AT; ++i)
+#pragma unroll
+    for (int j = 0; j < BT; ++j) acc[i][j] = (floatx4_t){0, 0, 0, 0};
+  const uint8_t *pa[AT], *pb[BT];
+  const int *ea[AT], *eb[BT];
+#pragma unroll
+  for (int i = 0; i < AT; ++i) {
+    const int64_t t = min(a0 + i, w.tiles - 1);
+    pa[i] = w.codes + t * w.tile_bytes;
+    ea[i] = (const int*)(w.exps + t * quads * 256) + lane;
+  }
+#pragma unroll
+  for (int j = 0; j < BT; ++j) {
+    const int64_t t = min(b0 + j, x.tiles - 1);
+    pb[j] = x.codes + t * x.tile_bytes;
+    eb[j] = (const int*)(x.exps + t * quads * 256) + lane;
+  }
+  for (int q = 0; q < quads; ++q) {
+    int sa[AT], sb[BT];
+#pragma unroll
+    for (int i = 0; i < AT; ++i) sa[i] = ea[i][q * 64];
+#pragma unroll
+    for (int j = 0; j < BT; ++j) sb[j] = eb[j][q * 64];
+    auto step = [&](auto J) {
+      constexpr int jj = decltype(J)::value;
+      const int64_t c = 4 * q + jj;
+      if (c >= chunks) return;
+      i32x8_t A[AT], B[BT];
+#pragma unroll
+      for (int i = 0; i < AT; ++i) A[i] = operand(pa[i] + c * 1024, lane, false);
+#pragma unroll
+      for (int j = 0; j < BT; ++j) B[j] = operand(pb[j] + c * (FMT ? 2048 : 1024), lane, FMT == kE4M3);
+#pragma unroll
+      for (int i = 0; i < AT; ++i)
+#pragma unroll
+        for (int j = 0; j < BT; ++j) acc[i][j] = mx_mfma<FMT, jj>(A[i], B[j], acc[i][j], sa[i], sb[j]);
+    };
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+    step(std::integral_constant<int, 2>{});
+    step(std::integral_constant<int, 3>{});
+  }
+#pragma unroll
+  for (int i = 0; i < AT; ++i)
+#pragma unroll
+    for (int j = 0; j < BT; ++j)
+      put4(ep, M, T, (a0 + i) * 16 + 4 * (lane >> 4), (b0 + j) * 16 + (lane & 15), acc[i][j]);
+}
+
+// ---- host side ----------------------------------------------------------------
+int hip_status(hipError_t e) {
+  if (e == hipSuccess) return QGEMV_OK;
+  qgemv_set_hip_error((int)e);
+  return QGEMV_ERR_HIP;
+}
+
+int check_shape(const qmx_shape* s) {
+  if (!s) return QGEMV_ERR_INVALID_ARG;
+  if (s->rows < 0 || s->cols < 1) return QGEMV_ERR_INVALID_ARG;
+  if (s->rows > kMaxRows || s->cols > kMaxCols || s->cols % 32) return QGEMV_ERR_UNSUPPORTED;
+  if (s->format != QMX_E2M1 && s->format != QMX_E4M3) return QGEMV_ERR_UNSUPPORTED;
+  const Geo g = geo(s->rows, s->cols, s->format);
+  // a wave a chunk, and fewer than 2^32 threads a launch
+  if ((int64_t)g.tiles * g.chunks > (1 << 26) - 4) return QGEMV_ERR_UNSUPPORTED;
+  return QGEMV_OK;
+}
+
+int check_rows(const void* x, int type, int64_t ldx) {
+  if (!x || (uintptr_t)x % 16 || ldx % 8) return QGEMV_ERR_INVALID_ARG;
+  if (type != QGEMV_F16 && type != QGEMV_F32) return QGEMV_ERR_UNSUPPORTED;
+  return QGEMV_OK;
+}
+
+bool bad_blocks(const void* p) { return !p || (uintptr_t)p % 256; }
+
+Side side(const void* blocks, const Geo& g) {
+  return Side{(const uint8_t*)blocks, (const uint8_t*)blocks + g.exps, g.tile_bytes, g.tiles};
+}
+
+hipError_t launch_quantize(const Geo& g, void* blocks, const void* x, int type, int64_t ldx, int clip, hipStream_t st) {
+  const int total = g.tiles * g.chunks;
+  auto go = [&](auto k) { hipLaunchKernelGGL(k, dim3((total + 3) / 4), dim3(256), 0, st, (uint8_t*)blocks, g, x, ldx, clip, total); };
+  if (g.fmt == QMX_E2M1) type == QGEMV_F32 ? go(k_mx_quantize<kE2M1, true>) : go(k_mx_quantize<kE2M1, false>);
+  else type == QGEMV_F32 ? go(k_mx_quantize<kE4M3, true>) : go(k_mx_quantize<kE4M3, false>);
+  return hipGetLastError();
+}
+
+struct RunPlan {
+  Geo gw, gx;
+  size_t x_bytes, bytes;
+};
+
+int run_plan(const qmx_shape* w, const qmx_input* x, const qgemv_epilogue* e, RunPlan& p) {
+  int st = check_shape(w);
+  if (st) return st;
+  if (!x || !e || w->rows < 1) return QGEMV_ERR_INVALID_ARG;
+  if (w->format != QMX_E2M1) return QGEMV_ERR_UNSUPPORTED;
+  const qmx_shape xs = {x->rows, w->cols, x->format};
+  if ((st = check_shape(&xs))) return st;
+  if (x->x_type != QMX_IN_BLOCKS && x->x_type != QGEMV_F16 && x->x_type != QGEMV_F32) return QGEMV_ERR_UNSUPPORTED;
+  p.gw = geo(w->rows, w->cols, w->format);
+  p.gx = geo(x->rows, w->cols, x->format);
+  p.x_bytes = x->x_type == QMX_IN_BLOCKS ? 0 : (size_t)p.gx.bytes;
+  p.bytes = p.x_bytes;
+  return QGEMV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int qmx_bytes(const qmx_shape* shape, size_t* bytes) {
+  const int st = check_shape(shape);
+  if (st) return st;
+  if (!bytes) return QGEMV_ERR_INVALID_ARG;
+  *bytes = (size_t)geo(shape->rows, shape->cols, shape->format).bytes;
+  return QGEMV_OK;
+}
+
+int qmx_quantize(const qmx_shape* shape, void* blocks, const void* x, int32_t x_type, int64_t ldx, int32_t clip,
+                 void* stream) {
+  int st = check_shape(shape);
+  if (st || shape->rows == 0) return st;
+  if (bad_blocks(blocks)) return QGEMV_ERR_INVALID_ARG;
+  if ((st = check_rows(x, x_type, ldx))) return st;
+  return hip_status(launch_quantize(geo(shape->rows, shape->cols, shape->format), blocks, x, x_type, ldx, clip != 0,
+                                    (hipStream_t)stream));
+}
+
+int qmx_values(const qmx_shape* shape, const void* blocks, void* x, int32_t x_type, int64_t ldx, void* stream) {
+  int st = check_shape(shape);
+  if (st || shape->rows == 0) return st;
+  if (bad_blocks(blocks)) return QGEMV_ERR_INVALID_ARG;
+  if ((st = check_rows(x, x_type, ldx))) return st;
+  if (shape->rows > 1 && ldx < shape->cols) return QGEMV_ERR_INVALID_ARG;
+  const Geo g = geo(shape->rows, shape->cols, shape->format);
+  const int total = g.tiles * g.chunks;
+  auto go = [&](auto k) {
+    hipLaunchKernelGGL(k, dim3((total + 3) / 4), dim3(256), 0, (hipStream_t)stream, (const uint8_t*)blocks, g, x, ldx, total);
+  };
+  if (g.fmt == QMX_E2M1) x_type == QGEMV_F32 ? go(k_mx_values<kE2M1, true>) : go(k_mx_values<kE2M1, false>);
+  else x_type == QGEMV_F32 ? go(k_mx_values<kE4M3, true>) : go(k_mx_values<kE4M3, false>);
+  return hip_status(hipGetLastError());
+}
+
+static int plain(const qmx_shape* shape, const void* blocks, const void* codes, const void* exponents, bool pack,
+                 void* stream) {
+  const int st = check_shape(shape);
+  if (st || shape->rows == 0) return st;
+  if (bad_blocks(blocks) || !codes || (uintptr_t)codes % 16 || !exponents) return QGEMV_ERR_INVALID_ARG;
+  const Geo g = geo(shape->rows, shape->cols, shape->format);
+  const int total = g.tiles * g.chunks;
+  auto go = [&](auto k) {
+    hipLaunchKernelGGL(k, dim3((total + 3) / 4), dim3(256), 0, (hipStream_t)stream, (uint8_t*)blocks, g, (uint8_t*)codes,
+                       (uint8_t*)exponents, total);
+  };
+  if (g.fmt == QMX_E2M1) pack ? go(k_mx_plain<kE2M1, true>) : go(k_mx_plain<kE2M1, false>);
+  else pack ? go(k_mx_plain<kE4M3, true>) : go(k_mx_plain<kE4M3, false>);
+  return hip_status(hipGetLastError());
+}
+
+int qmx_pack(const qmx_shape* shape, void* blocks, const void* codes, const void* exponents, void* stream) {
+  return plain(shape, blocks, codes, exponents, true, stream);
+}
+
+int qmx_unpack(const qmx_shape* shape, const void* blocks, void* codes, void* exponents, void* stream) {
+  return plain(shape, blocks, codes, exponents, false, stream);
+}
+
+int qmx_run_ws(const qmx_shape* w, const qmx_input* x, const qgemv_epilogue* e, size_t* bytes) {
+  RunPlan p;
+  const int st = run_plan(w, x, e, p);
+  if (st) return st;
+  if (!bytes) return QGEMV_ERR_INVALID_ARG;
+  *bytes = p.bytes;
+  return QGEMV_OK;
+}
+
+int qmx_run(const qmx_shape* w, const void* w_blocks, const qmx_input* x, void* y, const qgemv_epilogue* e, void* ws,
+            size_t ws_bytes, void* stream) {
+  RunPlan p;
+  int st = run_plan(w, x, e, p);
+  if (st || x->rows == 0) return st;
+  if (bad_blocks(w_blocks) || !y) return QGEMV_ERR_INVALID_ARG;
+  EpiArg<true> ep;
+  if ((st = fill_epilogue(w->rows, y, e, ep))) return st;
+  const void* xb = x->data;
+  if (x->x_type == QMX_IN_BLOCKS) {
+    if (bad_blocks(xb)) return QGEMV_ERR_INVALID_ARG;
+  } else if ((st = check_rows(xb, x->x_type, x->ldx))) {
+    return st;
+  }
+  if (p.bytes > 0 && (!ws || (uintptr_t)ws % 256)) return QGEMV_ERR_INVALID_ARG;
+  if (ws_bytes < p.bytes) return QGEMV_ERR_SIZE;
+  const hipStream_t s = (hipStream_t)stream;
+  if (x->x_type != QMX_IN_BLOCKS) {
+    const hipError_t er = launch_quantize(p.gx, ws, xb, x->x_type, x->ldx, 0, s);
+    if (er != hipSuccess) return hip_status(er);
+    xb = ws;
+  }
+  const Side a = side(w_blocks, p.gw), b = side(xb, p.gx);
+  const dim3 grid((a.tiles + 7) / 8, (b.tiles + 1) / 2);
+  if (p.gx.fmt == QMX_E2M1) hipLaunchKernelGGL(k_mx_simple<kE2M1>, grid, dim3(256), 0, s, a, b, ep, w->rows, x->rows, p.gw.chunks, p.gw.quads);
+  else hipLaunchKernelGGL(k_mx_simple<kE4M3>, grid, dim3(256), 0, s, a, b, ep, w->rows, x->rows, p.gw.chunks, p.gw.quads);
+  return hip_status(hipGetLastError());
+}
+
+}  // extern "C"
