@@ -27,6 +27,12 @@ __device__ __forceinline__ float mx_step(uint32_t byte) {
   return __uint_as_float(byte == 255 ? 0x7FC00000u : byte == 0 ? 0x00400000u : byte << 23);
 }
 
+// Byte offset in a chunk of the 8 elements of row r (of 16), columns 8 c .. + 7 of the chunk.
+template <int FMT>
+__device__ __forceinline__ int lane_bytes(int r, int c) {
+  return FMT == kE2M1 ? 16 * (16 * (c >> 2) + r) + 4 * (c & 3) : 1024 * (c >> 3) + 16 * (16 * ((c >> 1) & 3) + r) + 8 * (c & 1);
+}
+
 // Four values times 2^-e in E4M3.  The conversion rounds to nearest even; what lies above the largest is held at it
 // beforehand.
 __device__ __forceinline__ uint32_t mx_four_e4m3(float a, float b, float c, float d) {

@@ -46,12 +46,6 @@ __device__ __forceinline__ void load8(const void* x, int64_t e, float (&v)[8]) {
   }
 }
 
-// Byte offset of the lane's elements of row r (of 16), columns 8 c .. + 7 of the chunk.
-template <int FMT>
-__device__ __forceinline__ int lane_bytes(int r, int c) {
-  return FMT == kE2M1 ? 16 * (16 * (c >> 2) + r) + 4 * (c & 3) : 1024 * (c >> 3) + 16 * (16 * ((c >> 1) & 3) + r) + 8 * (c & 1);
-}
-
 template <int FMT, bool F32>
 __global__ void __launch_bounds__(256)
 k_mx_quantize(uint8_t* __restrict__ blocks, Geo g, const void* __restrict__ x, int64_t ldx, int clip, int total) {
@@ -184,9 +178,42 @@ __device__ __forceinline__ i32x8_t operand(const uint8_t* p, int lane, bool two)
   return (i32x8_t){(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
 
+// An operand of E4M3 elements in its upper and its lower eight binades.  The scaled MFMA adds E4M3 products with fewer bits
+// than fp32 has below the largest: with all sixteen binades in one operand, sums came out up to 1e-4 of the largest
+// product off (2e-5 of an output's 2-norm); eight at a time add up exactly.
+template <int FMT>
+struct Tokens {
+  i32x8_t v;
+};
+template <>
+struct Tokens<kE4M3> {
+  i32x8_t v, lo;
+};
+template <int FMT>
+__device__ __forceinline__ Tokens<FMT> tokens(i32x8_t x) {
+  Tokens<FMT> t;
+  if constexpr (FMT == kE2M1) {
+    t.v = x;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t m = ((uint32_t)x[i] & 0x40404040u) >> 6;
+      const uint32_t mask = (m << 8) - m;  // 0xFF where the top exponent bit is set
+      t.v[i] = x[i] & (int)mask;
+      t.lo[i] = x[i] & (int)~mask;
+    }
+  }
+  return t;
+}
+
 template <int FMT, int J>
-__device__ __forceinline__ floatx4_t mx_mfma(i32x8_t a, i32x8_t b, floatx4_t c, int ea, int eb) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, FMT == kE2M1 ? 4 : 0, J, ea, J, eb);
+__device__ __forceinline__ floatx4_t mx_mfma(i32x8_t a, const Tokens<FMT>& b, floatx4_t c, int ea, int eb) {
+  if constexpr (FMT == kE2M1) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b.v, c, 4, 4, J, ea, J, eb);
+  } else {
+    c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b.lo, c, 4, 0, J, ea, J, eb);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b.v, c, 4, 0, J, ea, J, eb);
+  }
 }
 
 // The lane's four features of one token.
@@ -239,11 +266,12 @@ k_mx_simple(Side w, Side x, EpiArg<true> ep, int M, int T, int chunks, int quads
       constexpr int jj = decltype(J)::value;
       const int64_t c = 4 * q + jj;
       if (c >= chunks) return;
-      i32x8_t A[AT], B[BT];
+      i32x8_t A[AT];
+      Tokens<FMT> B[BT];
 #pragma unroll
       for (int i = 0; i < AT; ++i) A[i] = operand(pa[i] + c * 1024, lane, false);
 #pragma unroll
-      for (int j = 0; j < BT; ++j) B[j] = operand(pb[j] + c * (FMT ? 2048 : 1024), lane, FMT == kE4M3);
+      for (int j = 0; j < BT; ++j) B[j] = tokens<FMT>(operand(pb[j] + c * (FMT ? 2048 : 1024), lane, FMT == kE4M3));
 #pragma unroll
       for (int i = 0; i < AT; ++i)
 #pragma unroll

@@ -1,0 +1,249 @@
+// qnorm_kernels.hip -- the norms after and before a block, fused with the gate
+// and the residual stream (include/qnorm.h).
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/qnorm.h"
+#include "qgemv_decode.h"
+#include "qgemv_internal.h"
+#include "qmx_blocks.h"
+#include "qmx_layout.h"
+
+using namespace qgemv_dev;
+using namespace qmx_dev;
+using qmx_layout::Geo;
+
+namespace {
+
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+typedef float floatx4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+struct Arr {
+  char* data;
+  int f32;
+  int64_t ld;
+};
+
+struct NormArgs {
+  Arr y, h, gate, post, post_bias, pre, pre_bias, h_out, out;
+  Geo g;  // out in blocks
+  int rows, cols;
+  float eps, scale, inv_n;
+};
+
+__device__ __forceinline__ void load8(const Arr& a, int64_t row, int col, float (&v)[8]) {
+  const int64_t e = row * a.ld + col;
+  if (a.f32) {
+    const floatx4_t* p = (const floatx4_t*)((const float*)a.data + e);
+    const floatx4_t x = p[0], y = p[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = x[i], v[4 + i] = y[i];
+  } else {
+    const half8_t x = *(const half8_t*)((const _Float16*)a.data + e);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (float)x[i];
+  }
+}
+__device__ __forceinline__ void store8(const Arr& a, int64_t row, int col, const float (&v)[8]) {
+  const int64_t e = row * a.ld + col;
+  if (a.f32) {
+    floatx4_t* p = (floatx4_t*)((float*)a.data + e);
+    p[0] = (floatx4_t){v[0], v[1], v[2], v[3]};
+    p[1] = (floatx4_t){v[4], v[5], v[6], v[7]};
+  } else {
+    half8_t x;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = (_Float16)v[i];
+    *(half8_t*)((_Float16*)a.data + e) = x;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// W waves take a row; a lane holds V runs of 8 columns of it in fp32 registers
+// from the first load to the last store, so every array is read or written
+// once.  Means and mean squares (of the centred values, so nothing cancels) are sums over the
+// lane, the wave, and the row's waves by way of LDS.
+// ---------------------------------------------------------------------------
+template <int W>
+__device__ __forceinline__ float row_sum(float v, float* s, int& turn, int wave) {
+  v = wave_sum(v);
+  if constexpr (W > 1) {
+    float* at = s + (turn ^= 16);  // the other half: the last sum may still be being read
+    if ((threadIdx.x & 63) == 0) at[wave] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) v += at[i];
+  }
+  return v;
+}
+
+// OUT: 0 rows, 1 E2M1, 2 E4M3.
+template <int W, int V, bool LAYER, int OUT>
+__global__ void __launch_bounds__(W == 1 ? 256 : 64 * W)
+k_qnorm(NormArgs a) {
+  __shared__ float s_sum[32];
+  int turn = 0;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row = W == 1 ? blockIdx.x * 4 + wave : blockIdx.x;
+  if (row >= a.rows) return;
+  const int first = 8 * (W == 1 ? lane : (int)threadIdx.x);
+  constexpr int step = 8 * 64 * W;
+  float x[V][8], h[V][8];
+  auto norm = [&](const Arr& weight, const Arr& bias) {
+    float mean = 0.f;
+    if constexpr (LAYER) {
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += x[j][i];
+      mean = row_sum<W>(sum, s_sum, turn, wave) * a.inv_n;
+    }
+    float sq = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (LAYER) x[j][i] = first + j * step < a.cols ? x[j][i] - mean : 0.f;
+        sq = __builtin_fmaf(x[j][i], x[j][i], sq);
+      }
+    const float r = 1.f / sqrtf(row_sum<W>(sq, s_sum, turn, wave) * a.inv_n + a.eps);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int col = first + j * step;
+      if (col >= a.cols) continue;
+      float w[8], b[8];
+      load8(weight, 0, col, w);
+      if (bias.data) load8(bias, 0, col, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float t = x[j][i] * r;
+        x[j][i] = bias.data ? __builtin_fmaf(t, w[i], b[i]) : t * w[i];
+      }
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int col = first + j * step;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[j][i] = h[j][i] = 0.f;
+    if (col >= a.cols) continue;
+    if (a.y.data) load8(a.y, row, col, x[j]);
+    if (a.h.data) load8(a.h, row, col, h[j]);
+  }
+  if (a.post.data) norm(a.post, a.post_bias);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int col = first + j * step;
+    if (col >= a.cols) continue;
+    if (a.gate.data) {
+      float gt[8];
+      load8(a.gate, row, col, gt);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[j][i] *= gt[i];
+    }
+    if (a.h.data) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[j][i] = a.y.data ? __builtin_fmaf(a.scale, h[j][i], x[j][i]) : a.scale * h[j][i];
+    }
+    if (a.h_out.data) store8(a.h_out, row, col, x[j]);
+  }
+  if (!a.pre.data) return;
+  norm(a.pre, a.pre_bias);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int col = first + j * step;
+    if constexpr (OUT == 0) {
+      if (col < a.cols) store8(a.out, row, col, x[j]);
+    } else {
+      // the columns up to the chunk's end are zeros
+      constexpr int F = OUT == 1 ? kE2M1 : kE4M3;
+      if (col >= 128 * a.g.chunks) continue;
+      uint32_t w[2];
+      const uint32_t byte = mx_quad<F>(x[j], false, w);
+      const int tile = row >> 4, r = row & 15, chunk = col >> 7, c = (col & 127) >> 3;
+      uint8_t* to = (uint8_t*)a.out.data + tile * a.g.tile_bytes + (int64_t)chunk * (F ? 2048 : 1024);
+      if constexpr (F == kE2M1) *(uint32_t*)(to + lane_bytes<F>(r, c)) = w[0];
+      else *(u32x2_t*)(to + lane_bytes<F>(r, c)) = (u32x2_t){w[0], w[1]};
+      if ((c & 3) == 0) {
+        uint8_t* ex = (uint8_t*)a.out.data + a.g.exps + ((int64_t)tile * a.g.quads + (chunk >> 2)) * 256 + (chunk & 3);
+        ex[4 * (16 * (c >> 2) + r)] = (uint8_t)byte;
+      }
+    }
+  }
+}
+
+// ---- host side ----------------------------------------------------------------
+template <int W, int V, bool LAYER>
+hipError_t launch(const NormArgs& a, int out, hipStream_t st) {
+  const int grid = W == 1 ? (a.rows + 3) / 4 : a.rows, threads = W == 1 ? 256 : 64 * W;
+  auto go = [&](auto k) { hipLaunchKernelGGL(k, dim3(grid), dim3(threads), 0, st, a); };
+  if (out == 0) go(k_qnorm<W, V, LAYER, 0>);
+  else if (out == 1) go(k_qnorm<W, V, LAYER, 1>);
+  else go(k_qnorm<W, V, LAYER, 2>);
+  return hipGetLastError();
+}
+template <bool LAYER>
+hipError_t by_size(const NormArgs& a, int out, hipStream_t st) {
+  const int n = a.cols;
+  if (n <= 512) return launch<1, 1, LAYER>(a, out, st);
+  if (n <= 2048) return launch<4, 1, LAYER>(a, out, st);
+  if (n <= 8192) return launch<4, 4, LAYER>(a, out, st);
+  return launch<16, 4, LAYER>(a, out, st);
+}
+
+int check_array(const qnorm_rows& r, bool vector) {
+  if (!r.data) return QGEMV_OK;
+  if (r.type != QGEMV_F16 && r.type != QGEMV_F32) return QGEMV_ERR_UNSUPPORTED;
+  if ((uintptr_t)r.data % 16 || (!vector && r.ld % 8)) return QGEMV_ERR_INVALID_ARG;
+  return QGEMV_OK;
+}
+Arr array(const qnorm_rows& r) { return Arr{(char*)r.data, r.type == QGEMV_F32, r.ld}; }
+
+}  // namespace
+
+extern "C" int qnorm_run(const qnorm_args* p, void* stream) {
+  if (!p) return QGEMV_ERR_INVALID_ARG;
+  if (p->rows < 0 || p->cols < 1) return QGEMV_ERR_INVALID_ARG;
+  if (p->rows > qmx_layout::kMaxRows || p->cols % 8 || p->cols > 32768) return QGEMV_ERR_UNSUPPORTED;
+  if (p->kind != QNORM_RMS && p->kind != QNORM_LAYER) return QGEMV_ERR_UNSUPPORTED;
+  if (!(p->eps >= 0.f) || !std::isfinite(p->eps) || !std::isfinite(p->scale)) return QGEMV_ERR_INVALID_ARG;
+  if (p->rows == 0) return QGEMV_OK;
+  const bool has_y = p->y.data, has_pre = p->pre.data, blocks = p->out.type == QNORM_OUT_E2M1 || p->out.type == QNORM_OUT_E4M3;
+  if ((!has_y && !p->h.data) || (!has_y && (p->gate.data || p->post.data))) return QGEMV_ERR_INVALID_ARG;
+  if ((p->post_bias.data && !p->post.data) || (p->pre_bias.data && !has_pre)) return QGEMV_ERR_INVALID_ARG;
+  if (has_pre != (p->out.data != nullptr) || (!p->out.data && !p->h_out.data)) return QGEMV_ERR_INVALID_ARG;
+  int st;
+  for (const qnorm_rows* r : {&p->y, &p->h, &p->gate, &p->h_out})
+    if ((st = check_array(*r, false))) return st;
+  for (const qnorm_rows* r : {&p->post, &p->post_bias, &p->pre, &p->pre_bias})
+    if ((st = check_array(*r, true))) return st;
+  if (p->rows > 1 && p->h_out.data && p->h_out.ld < p->cols) return QGEMV_ERR_INVALID_ARG;
+  NormArgs a{};
+  int out = 0;
+  if (has_pre && blocks) {
+    if ((uintptr_t)p->out.data % 256) return QGEMV_ERR_INVALID_ARG;
+    const qmx_shape s = {p->rows, p->cols, p->out.type - QNORM_OUT_E2M1};
+    size_t n;
+    if ((st = qmx_bytes(&s, &n))) return st;
+    a.g = qmx_layout::geo(s.rows, s.cols, s.format);
+    out = 1 + s.format;
+  } else if (has_pre) {
+    if ((st = check_array(p->out, false))) return st;
+    if (p->rows > 1 && p->out.ld < p->cols) return QGEMV_ERR_INVALID_ARG;
+  }
+  a.y = array(p->y), a.h = array(p->h), a.gate = array(p->gate), a.h_out = array(p->h_out), a.out = array(p->out);
+  a.post = array(p->post), a.post_bias = array(p->post_bias), a.pre = array(p->pre), a.pre_bias = array(p->pre_bias);
+  a.rows = p->rows, a.cols = p->cols, a.eps = p->eps, a.scale = p->scale;
+  a.inv_n = 1.f / (float)p->cols;
+  const hipError_t e = p->kind == QNORM_LAYER ? by_size<true>(a, out, (hipStream_t)stream)
+                                              : by_size<false>(a, out, (hipStream_t)stream);
+  if (e == hipSuccess) return QGEMV_OK;
+  qgemv_set_hip_error((int)e);
+  return QGEMV_ERR_HIP;
+}

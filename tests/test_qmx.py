@@ -264,6 +264,24 @@ def test_product(torch, T, M, K, fmt, rows):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,M,K", [(1, 48, 1024), (20, 64, 4096), (140, 144, 992)])
+def test_product_of_wide_ranges(torch, T, M, K, fmt):
+    """Every element of the formats, and powers of two 2^40 apart within a row: sums keep fp32's accuracy."""
+    rng = np.random.default_rng(K)
+    wc = rng.integers(0, 16, (M, K)).astype(np.uint8)
+    we = rng.integers(107, 148, (M, K // 32)).astype(np.uint8)
+    xc = rng.integers(0, 16 if fmt == "e2m1" else 256, (T, K)).astype(np.uint8)
+    xc[xc % 128 == 127] -= 1
+    xe = rng.integers(107, 148, (T, K // 32)).astype(np.uint8)
+    gpu = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    plan = qmx.QMx(qmx.MxRows.pack(gpu(mx.pack_bytes(wc, "e2m1")), gpu(we)))
+    x = qmx.MxRows.pack(gpu(mx.pack_bytes(xc, fmt)), gpu(xe), fmt)
+    want, tol = mx.product(mx.values(xc, xe, fmt), mx.values(wc, we, "e2m1"))
+    check(plan.run(x, dtype=torch.float32), want, tol, True)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("T,M,K", [(1, 96, 256), (16, 130, 512), (19, 70, 352), (70, 522, 1024), (260, 514, 640)])
