@@ -23,6 +23,10 @@ typedef float floatx4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef float floatx16_t __attribute__((ext_vector_type(16)));
+typedef float floatx2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 
 // ---------------------------------------------------------------------------
 // Quantising, and the values back.
@@ -216,6 +220,17 @@ __device__ __forceinline__ floatx4_t mx_mfma(i32x8_t a, const Tokens<FMT>& b, fl
   }
 }
 
+// The same of 32 features x 32 tokens and 64 columns.
+template <int FMT, int J>
+__device__ __forceinline__ floatx16_t mx_mfma32(i32x8_t a, const Tokens<FMT>& b, floatx16_t c, int ea, int eb) {
+  if constexpr (FMT == kE2M1) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b.v, c, 4, 4, J, ea, J, eb);
+  } else {
+    c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b.lo, c, 4, 0, J, ea, J, eb);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b.v, c, 4, 0, J, ea, J, eb);
+  }
+}
+
 // The lane's four features of one token.
 __device__ __forceinline__ void put4(const EpiArg<true>& ep, int M, int T, int row, int t, floatx4_t s) {
   if (t >= T) return;
@@ -289,6 +304,254 @@ k_mx_simple(Side w, Side x, EpiArg<true> ep, int M, int T, int chunks, int quads
       put4(ep, M, T, (a0 + i) * 16 + 4 * (lane >> 4), (b0 + j) * 16 + (lane & 15), acc[i][j]);
 }
 
+// ---------------------------------------------------------------------------
+// Many rows: a workgroup of four waves takes 64 AT features x 64 BT tokens, a wave
+// a quarter of them, 32 AT x 32 BT, in AT BT results of sixteen registers.
+//
+// 32x32x64 MFMAs: with E2M1 on both sides they run at 6.2 to 6.7 PFLOP/s on random
+// operands in registers (9.8 on zeros: the card's power decides), 16x16x128 at 4.4
+// to 5.1.  Their operand of 32 rows and half a chunk is 256 contiguous bytes of two tiles each.
+//
+// Chunks move from memory into LDS past the registers, S steps of 128 columns
+// ahead, as they are: a KiB a wave instruction; a wave's read of an operand is a KiB too,
+// without bank conflicts.  Operands are read from LDS half a chunk ahead.  One
+// barrier a chunk: behind it the next chunk has landed for all waves, and the place of the
+// one whose operands all waves hold is free.
+// ---------------------------------------------------------------------------
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+
+__device__ __forceinline__ rsrc_t resource(const uint8_t* p, int64_t bytes) {
+  const uint32_t n = bytes > 0xFFFFFFF0ll ? 0xFFFFFFF0u : (uint32_t)bytes;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), (short)0, (int)n, 0x00020000);
+}
+__device__ __forceinline__ void to_lds(rsrc_t r, uint8_t* dst, int voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, voff, soff, 0, 0);
+}
+// s_waitcnt vmcnt(N) alone.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
+}
+__device__ __forceinline__ void wait_lgkm() { __builtin_amdgcn_s_waitcnt(0xC07F); }
+__device__ __forceinline__ void wave_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Four neighbouring features of a token, from row (a multiple of 4) on, stored together where whole and aligned.
+__device__ __forceinline__ void put_four(const EpiArg<true>& ep, int M, int t, int row, floatx4_t v, bool whole) {
+  if (ep.bias) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = ep.biased(v[i], min(row + i, M - 1));
+  }
+  const int n = ep.gated ? 2 : 4;  // outputs
+  if (ep.gated) {
+    v[0] = ep.activate(v[0]) * v[1];
+    v[1] = ep.activate(v[2]) * v[3];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = ep.activate(v[i]);
+  }
+  const int col = ep.gated ? row >> 1 : row, mo = ep.gated ? M >> 1 : M;
+  if (!whole || col + n > mo) {
+    for (int i = 0; i < n; ++i)
+      if (col + i < mo) ep.store(t, col + i, i == 0 ? v[0] : i == 1 ? v[1] : i == 2 ? v[2] : v[3]);
+    return;
+  }
+  if (ep.residual) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) v[i] += ep.load(ep.residual, ep.res32, t * ep.ldr + col + i);
+  }
+  const int64_t e = t * ep.ldy + col;
+  if (ep.y32) {
+    float* y = (float*)ep.y + e;
+    if (ep.gated) *(floatx2_t*)y = (floatx2_t){v[0], v[1]};
+    else *(floatx4_t*)y = v;
+  } else {
+    _Float16* y = (_Float16*)ep.y + e;
+    const half4_t h = {(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+    if (ep.gated) *(half2_t*)y = (half2_t){h[0], h[1]};
+    else *(half4_t*)y = h;
+  }
+}
+
+// A wave's 16 AT features x 16 NT tokens, at `s` in LDS token by token (stride 16 AT + 4), to y.
+template <int AT, int NT>
+__device__ __forceinline__ void put_tile(const EpiArg<true>& ep, int M, int T, int row0, int t0, const float* s, int lane,
+                                         bool whole) {
+  constexpr int LT = 4 * AT, RT = 64 / LT;  // lanes of a token, tokens of a round
+  const int row = row0 + 4 * (lane % LT);
+  if (row >= M) return;
+#pragma unroll 1
+  for (int i = lane / LT; i < 16 * NT; i += RT) {
+    if (t0 + i >= T) return;
+    put_four(ep, M, t0 + i, row, *(const floatx4_t*)(s + i * (16 * AT + 4) + 4 * (lane % LT)), whole);
+  }
+}
+
+template <int FMT, int AT, int BT, int S>
+__global__ void __launch_bounds__(256, 1)
+k_mx_tile(Side w, Side x, EpiArg<true> ep, int M, int T, int chunks, int quads, int tiles_a, int tiles_b, bool whole) {
+  constexpr int P = FMT ? 2 : 1;               // KiB of a token chunk
+  constexpr int CA = 4 * AT, CB = 4 * BT * P;  // KiB of a stage
+  constexpr int NL = (CA + CB) / 4;            // copies of a wave and stage
+  constexpr int H = 2;                         // the results leave by way of LDS in H parts
+  extern __shared__ __align__(16) uint8_t lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int id = blockIdx.x;
+  const int ta = id % tiles_a, tb = id / tiles_a;
+  const int wa = wave & 1, wb = wave >> 1;
+  const int a0 = ta * 4 * AT, b0 = tb * 4 * BT;  // first tiles of 16
+  const rsrc_t ra = resource(w.codes + a0 * w.tile_bytes, (w.tiles - a0) * w.tile_bytes);
+  const rsrc_t rb = resource(x.codes + b0 * x.tile_bytes, (x.tiles - b0) * x.tile_bytes);
+  // the wave's copies: NL consecutive KiB of the stage; tiles past the last are the last again
+  int voff[NL];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int c = wave * NL + i;
+    voff[i] = c < CA ? min(c, w.tiles - 1 - a0) * (int)w.tile_bytes
+                     : min((c - CA) / P, x.tiles - 1 - b0) * (int)x.tile_bytes + (c - CA) % P * 1024;
+    voff[i] += 16 * lane;
+  }
+  auto stage = [&](int c) {
+    uint8_t* to = lds + (c % S) * ((CA + CB) * 1024) + wave * (NL * 1024);
+    const int cc = min(c, chunks - 1);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      if (wave * NL + i < CA) to_lds(ra, to + 1024 * i, voff[i], cc * 1024);
+      else to_lds(rb, to + 1024 * i, voff[i], cc * (1024 * P));
+    }
+  };
+  floatx16_t acc[AT][BT];
+#pragma unroll
+  for (int i = 0; i < AT; ++i)
+#pragma unroll
+    for (int j = 0; j < BT; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+  // Lane 32 g + n of an operand holds row n of two tiles; its blocks are g and 2 + g of a chunk.
+  const int tile = (lane >> 4) & 1, place = 16 * (lane & 15) + 256 * (lane >> 5);
+  const int* ea = (const int*)(w.exps + (place >> 2));
+  const int* eb = (const int*)(x.exps + (place >> 2));
+  int oa[AT], ob[BT];
+#pragma unroll
+  for (int i = 0; i < AT; ++i) oa[i] = min(a0 + 2 * (wa * AT + i) + tile, w.tiles - 1) * quads * 64;
+#pragma unroll
+  for (int j = 0; j < BT; ++j) ob[j] = min(b0 + 2 * (wb * BT + j) + tile, x.tiles - 1) * quads * 64;
+  int sa[2][AT], sb[2][BT], na[2][AT], nb[2][BT];
+  auto exponents = [&](int q) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < AT; ++i) na[h][i] = ea[oa[i] + q * 64 + 32 * h];
+#pragma unroll
+      for (int j = 0; j < BT; ++j) nb[h][j] = eb[ob[j] + q * 64 + 32 * h];
+    }
+  };
+  auto next_exponents = [&] {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < AT; ++i) sa[h][i] = na[h][i];
+#pragma unroll
+      for (int j = 0; j < BT; ++j) sb[h][j] = nb[h][j];
+    }
+  };
+  u32x4_t fa[2][AT], fb[2][BT][P];
+  const uint8_t* my_a = lds + (2 * wa * AT + tile) * 1024 + place;
+  const uint8_t* my_b = lds + (CA + (2 * wb * BT + tile) * P) * 1024 + place;
+  auto read = [&](int c, auto HH) {
+    constexpr int h = decltype(HH)::value;
+    const int at = (c % S) * ((CA + CB) * 1024);
+#pragma unroll
+    for (int i = 0; i < AT; ++i) fa[h][i] = *(const u32x4_t*)(my_a + at + 2048 * i + 512 * h);
+#pragma unroll
+    for (int j = 0; j < BT; ++j) {
+      // E4M3: columns 16 g .. and 32 + 16 g .. of part h
+      const uint8_t* p = my_b + at + 2048 * P * j + (P == 1 ? 512 : 1024) * h;
+#pragma unroll
+      for (int e = 0; e < P; ++e) fb[h][j][e] = *(const u32x4_t*)(p + 512 * e);
+    }
+  };
+  auto multiply = [&](auto HH, auto J) {
+    constexpr int h = decltype(HH)::value, jj = decltype(J)::value;
+#pragma unroll
+    for (int j = 0; j < BT; ++j) {
+      i32x8_t b = {};
+#pragma unroll
+      for (int e = 0; e < 4 * P; ++e) b[e] = (int)fb[h][j][e / 4][e % 4];
+      const Tokens<FMT> tk = tokens<FMT>(b);
+#pragma unroll
+      for (int i = 0; i < AT; ++i) {
+        const u32x4_t v = fa[h][i];
+        const i32x8_t a = {(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+        acc[i][j] = mx_mfma32<FMT, jj>(a, tk, acc[i][j], sa[h][i], sb[h][j]);
+      }
+    }
+  };
+  typedef std::integral_constant<int, 0> I0;
+  typedef std::integral_constant<int, 1> I1;
+  typedef std::integral_constant<int, 2> I2;
+  typedef std::integral_constant<int, 3> I3;
+  auto step = [&](auto J, int q) {
+    constexpr int jj = decltype(J)::value;
+    const int c = 4 * q + jj;
+    read(c, I1{});
+    multiply(I0{}, J);
+    // The next chunk has landed; on the way since then are S - 2 stages, and the next exponents.
+    wait_vm<(S - 2) * NL + (jj >= 1 && jj < S ? 2 * (AT + BT) : 0)>();
+    wait_lgkm();  // the chunk's operands are in registers, its place is free for all behind the barrier
+    wave_barrier();
+    stage(c + S);
+    if constexpr (jj == 0) exponents(min(q + 1, quads - 1));
+    read(c + 1, I0{});
+    multiply(I1{}, J);
+  };
+  exponents(0);
+#pragma unroll
+  for (int c = 0; c < S; ++c) stage(c);
+  wait_vm<(S - 1) * NL>();
+  wave_barrier();
+  read(0, I0{});
+  const int full = chunks >> 2, left = chunks & 3;
+  for (int q = 0; q < full; ++q) {
+    next_exponents();
+    step(I0{}, q);
+    step(I1{}, q);
+    step(I2{}, q);
+    step(I3{}, q);
+  }
+  if (left) {
+    next_exponents();
+    step(I0{}, full);
+    if (left > 1) step(I1{}, full);
+    if (left > 2) step(I2{}, full);
+  }
+  wait_vm<0>();  // copies past the end
+  wait_lgkm();
+  wave_barrier();
+  // Lane 32 g + n of a result holds features 8 u + 4 g .. + 3, u = 0 .. 3, of token n.
+  float* mine = (float*)lds + wave * (32 * BT / H * (32 * AT + 4));
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+#pragma unroll
+    for (int j = 0; j < BT / H; ++j)
+#pragma unroll
+      for (int i = 0; i < AT; ++i)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const floatx16_t& r = acc[i][h * (BT / H) + j];
+          *(floatx4_t*)(mine + (32 * j + (lane & 31)) * (32 * AT + 4) + 32 * i + 8 * u + 4 * (lane >> 5)) =
+              (floatx4_t){r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]};
+        }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    put_tile<2 * AT, 2 * BT / H>(ep, M, T, (a0 + 2 * wa * AT) * 16, (b0 + 2 * wb * BT + h * (2 * BT / H)) * 16, mine, lane, whole);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+}
+
 // ---- host side ----------------------------------------------------------------
 int hip_status(hipError_t e) {
   if (e == hipSuccess) return QGEMV_OK;
@@ -345,6 +608,33 @@ int run_plan(const qmx_shape* w, const qmx_input* x, const qgemv_epilogue* e, Ru
   p.x_bytes = x->x_type == QMX_IN_BLOCKS ? 0 : (size_t)p.gx.bytes;
   p.bytes = p.x_bytes;
   return QGEMV_OK;
+}
+
+template <class F>
+void lds_limit(F k, int bytes) {
+  (void)hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+// Whether groups of four outputs (two when gated) can be stored together.
+bool whole_fours(const EpiArg<true>& ep) {
+  const int n = ep.gated ? 2 : 4, size = ep.y32 ? 4 : 2;
+  return ep.ldy % n == 0 && (uintptr_t)ep.y % (n * size) == 0;
+}
+
+template <int FMT>
+hipError_t launch_product(const RunPlan& p, const Side& a, const Side& b, const EpiArg<true>& ep, hipStream_t st) {
+  const int M = p.gw.rows, T = p.gx.rows, ch = p.gw.chunks, qu = p.gw.quads;
+  if (T >= 256) {
+    constexpr int S = FMT ? 3 : 4, ring = S * (16 + 16 * (FMT ? 2 : 1)) * 1024, out = 4 * 64 * (128 + 4) * 4;
+    constexpr int lds = ring > out ? ring : out;
+    const int na = (a.tiles + 15) / 16, nb = (b.tiles + 15) / 16;
+    auto k = k_mx_tile<FMT, 4, 4, S>;
+    lds_limit(k, lds);
+    hipLaunchKernelGGL(k, dim3(na * nb), dim3(256), lds, st, a, b, ep, M, T, ch, qu, na, nb, whole_fours(ep));
+  } else {
+    hipLaunchKernelGGL(k_mx_simple<FMT>, dim3((a.tiles + 7) / 8, (b.tiles + 1) / 2), dim3(256), 0, st, a, b, ep, M, T, ch, qu);
+  }
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -441,10 +731,6 @@ int qmx_run(const qmx_shape* w, const void* w_blocks, const qmx_input* x, void* 
     xb = ws;
   }
   const Side a = side(w_blocks, p.gw), b = side(xb, p.gx);
-  const dim3 grid((a.tiles + 7) / 8, (b.tiles + 1) / 2);
-  if (p.gx.fmt == QMX_E2M1) hipLaunchKernelGGL(k_mx_simple<kE2M1>, grid, dim3(256), 0, s, a, b, ep, w->rows, x->rows, p.gw.chunks, p.gw.quads);
-  else hipLaunchKernelGGL(k_mx_simple<kE4M3>, grid, dim3(256), 0, s, a, b, ep, w->rows, x->rows, p.gw.chunks, p.gw.quads);
-  return hip_status(hipGetLastError());
+  return hip_status(p.gx.fmt == QMX_E2M1 ? launch_product<kE2M1>(p, a, b, ep, s) : launch_product<kE4M3>(p, a, b, ep, s));
 }
-
 }  // extern "C"
