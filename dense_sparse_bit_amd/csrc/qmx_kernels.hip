@@ -24,9 +24,7 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef float floatx16_t __attribute__((ext_vector_type(16)));
-typedef float floatx2_t __attribute__((ext_vector_type(2)));
-typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
-typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
+typedef float floatx1_t __attribute__((ext_vector_type(1)));
 
 // ---------------------------------------------------------------------------
 // Quantising, and the values back.
@@ -339,56 +337,117 @@ __device__ __forceinline__ void wave_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// Four neighbouring features of a token, from row (a multiple of 4) on, stored together where whole and aligned.
-__device__ __forceinline__ void put_four(const EpiArg<true>& ep, int M, int t, int row, floatx4_t v, bool whole) {
-  if (ep.bias) {
+// N values activated under one look at the kind.
+template <int N>
+__device__ __forceinline__ void activate_all(const EpiArg<true>& ep, float (&v)[N]) {
+  if (ep.act == QGEMV_ACT_NONE) return;
+  if (ep.act == QGEMV_ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = ep.biased(v[i], min(row + i, M - 1));
-  }
-  const int n = ep.gated ? 2 : 4;  // outputs
-  if (ep.gated) {
-    v[0] = ep.activate(v[0]) * v[1];
-    v[1] = ep.activate(v[2]) * v[3];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = ep.activate(v[i]);
-  }
-  const int col = ep.gated ? row >> 1 : row, mo = ep.gated ? M >> 1 : M;
-  if (!whole || col + n > mo) {
-    for (int i = 0; i < n; ++i)
-      if (col + i < mo) ep.store(t, col + i, i == 0 ? v[0] : i == 1 ? v[1] : i == 2 ? v[2] : v[3]);
+    for (int i = 0; i < N; ++i) v[i] = v[i] / (1.f + expf(-v[i]));
     return;
   }
-  if (ep.residual) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) v[i] += ep.load(ep.residual, ep.res32, t * ep.ldr + col + i);
-  }
-  const int64_t e = t * ep.ldy + col;
-  if (ep.y32) {
-    float* y = (float*)ep.y + e;
-    if (ep.gated) *(floatx2_t*)y = (floatx2_t){v[0], v[1]};
-    else *(floatx4_t*)y = v;
+  for (int i = 0; i < N; ++i) v[i] = ep.activate(v[i]);
+}
+
+template <class V>
+__device__ __forceinline__ void put_typed(void* y, int f32, int64_t e, V v) {
+  constexpr int n = sizeof(V) / 4;
+  if (f32) {
+    *(V*)((float*)y + e) = v;
   } else {
-    _Float16* y = (_Float16*)ep.y + e;
-    const half4_t h = {(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
-    if (ep.gated) *(half2_t*)y = (half2_t){h[0], h[1]};
-    else *(half4_t*)y = h;
+    typedef _Float16 hv __attribute__((ext_vector_type(n)));
+    *(hv*)((_Float16*)y + e) = __builtin_convertvector(v, hv);
   }
 }
 
-// A wave's 16 AT features x 16 NT tokens, at `s` in LDS token by token (stride 16 AT + 4), to y.
+// A wave's 16 AT features x 16 NT tokens, at `s` in LDS token by token (stride 16 AT + 4), to y: a lane takes eight
+// features of a token, U tokens at a time so that their reads and stores overlap.
 template <int AT, int NT>
 __device__ __forceinline__ void put_tile(const EpiArg<true>& ep, int M, int T, int row0, int t0, const float* s, int lane,
                                          bool whole) {
-  constexpr int LT = 4 * AT, RT = 64 / LT;  // lanes of a token, tokens of a round
-  const int row = row0 + 4 * (lane % LT);
+  constexpr int LT = 2 * AT, RT = 64 / LT;  // lanes of a token, tokens of a round
+  constexpr int U = 4;
+  const int f = 8 * (lane % LT), row = row0 + f;
   if (row >= M) return;
+  float bias[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) bias[i] = ep.bias ? ep.load(ep.bias, ep.bias32, min(row + i, M - 1)) : 0.f;
+  const int mo = ep.gated ? M >> 1 : M, col = ep.gated ? row >> 1 : row;
+  const int n = min(ep.gated ? 4 : 8, mo - col);
+  const bool full = whole && n == (ep.gated ? 4 : 8);
 #pragma unroll 1
-  for (int i = lane / LT; i < 16 * NT; i += RT) {
-    if (t0 + i >= T) return;
-    put_four(ep, M, t0 + i, row, *(const floatx4_t*)(s + i * (16 * AT + 4) + 4 * (lane % LT)), whole);
+  for (int i0 = lane / LT; i0 < 16 * NT && t0 + i0 < T; i0 += U * RT) {
+    float g[U * 8];  // features, or gates
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float* at = s + min(i0 + u * RT, 16 * NT - 1) * (16 * AT + 4) + f;
+      const floatx4_t a = *(const floatx4_t*)at, b = *(const floatx4_t*)(at + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) g[8 * u + i] = a[i] + bias[i], g[8 * u + 4 + i] = b[i] + bias[4 + i];
+    }
+    if (ep.gated) {
+      float h[U * 4];
+#pragma unroll
+      for (int i = 0; i < U * 4; ++i) h[i] = g[2 * i];
+      activate_all(ep, h);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) g[8 * u + i] = h[4 * u + i] * g[8 * u + 2 * i + 1];
+    } else {
+      activate_all(ep, g);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * RT, t = t0 + i;
+      if (i >= 16 * NT || t >= T) continue;
+      const int64_t e = t * ep.ldy + col, er = t * ep.ldr + col;
+      if (ep.residual) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < n) g[8 * u + k] += ep.load(ep.residual, ep.res32, er + k);
+      }
+      const floatx4_t a = {g[8 * u], g[8 * u + 1], g[8 * u + 2], g[8 * u + 3]};
+      const floatx4_t b = {g[8 * u + 4], g[8 * u + 5], g[8 * u + 6], g[8 * u + 7]};
+      if (full && ep.gated) {
+        put_typed(ep.y, ep.y32, e, a);
+      } else if (full && ep.y32) {
+        put_typed(ep.y, 1, e, a);
+        put_typed(ep.y, 1, e + 4, b);
+      } else if (full) {
+        *(half8_t*)((_Float16*)ep.y + e) = __builtin_convertvector(__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7), half8_t);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < n) put_typed(ep.y, ep.y32, e + k, (floatx1_t){g[8 * u + k]});
+      }
+    }
   }
+}
+
+// The order of a half chunk's instructions: an LDS read (and, with VM, a copy) between every few MFMAs.  Left to itself the
+// compiler moves the reads down to their use, and waits for each.
+template <int READS, int MFMAS, int VM>
+__device__ __forceinline__ void spread() {
+  constexpr int per = MFMAS / READS;
+#pragma unroll
+  for (int i = 0; i < READS; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    if constexpr (VM) __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x8, per, 0);
+  }
+}
+
+// Workgroups go to the eight XCDs in turn.  Each XCD takes a contiguous part of the tiles, in an order that walks four token
+// tiles and then on to the next features: its 32 CUs are at work on some 4 x 8 tiles, whose operands its L2
+// shares.
+__device__ __forceinline__ void tile_of(int id, int tiles_a, int tiles_b, int& ta, int& tb) {
+  const int n = tiles_a * tiles_b, q = n >> 3, r = n & 7, xcd = id & 7;
+  const int t = xcd * q + min(xcd, r) + (id >> 3);
+  const int per = 4 * tiles_a, grp = t / per, in = t - grp * per, width = min(4, tiles_b - 4 * grp);
+  ta = in / width;
+  tb = 4 * grp + in - ta * width;
 }
 
 template <int FMT, int AT, int BT, int S>
@@ -400,8 +459,8 @@ k_mx_tile(Side w, Side x, EpiArg<true> ep, int M, int T, int chunks, int quads, 
   constexpr int H = 2;                         // the results leave by way of LDS in H parts
   extern __shared__ __align__(16) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int id = blockIdx.x;
-  const int ta = id % tiles_a, tb = id / tiles_a;
+  int ta, tb;
+  tile_of(blockIdx.x, tiles_a, tiles_b, ta, tb);
   const int wa = wave & 1, wb = wave >> 1;
   const int a0 = ta * 4 * AT, b0 = tb * 4 * BT;  // first tiles of 16
   const rsrc_t ra = resource(w.codes + a0 * w.tile_bytes, (w.tiles - a0) * w.tile_bytes);
@@ -498,8 +557,11 @@ k_mx_tile(Side w, Side x, EpiArg<true> ep, int M, int T, int chunks, int quads, 
   auto step = [&](auto J, int q) {
     constexpr int jj = decltype(J)::value;
     const int c = 4 * q + jj;
+    __builtin_amdgcn_sched_barrier(0);
     read(c, I1{});
     multiply(I0{}, J);
+    spread<AT + BT * P, AT * BT * P, 0>();
+    __builtin_amdgcn_sched_barrier(0);
     // The next chunk has landed; on the way since then are S - 2 stages, and the next exponents.
     wait_vm<(S - 2) * NL + (jj >= 1 && jj < S ? 2 * (AT + BT) : 0)>();
     wait_lgkm();  // the chunk's operands are in registers, its place is free for all behind the barrier
@@ -508,6 +570,7 @@ k_mx_tile(Side w, Side x, EpiArg<true> ep, int M, int T, int chunks, int quads, 
     if constexpr (jj == 0) exponents(min(q + 1, quads - 1));
     read(c + 1, I0{});
     multiply(I1{}, J);
+    spread<AT + BT * P, AT * BT * P, 1>();
   };
   exponents(0);
 #pragma unroll
@@ -615,9 +678,9 @@ void lds_limit(F k, int bytes) {
   (void)hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-// Whether groups of four outputs (two when gated) can be stored together.
-bool whole_fours(const EpiArg<true>& ep) {
-  const int n = ep.gated ? 2 : 4, size = ep.y32 ? 4 : 2;
+// Whether a lane's eight outputs (four when gated) can be stored together, 16 bytes or the whole at a time.
+bool whole_rows(const EpiArg<true>& ep) {
+  const int n = ep.gated || ep.y32 ? 4 : 8, size = ep.y32 ? 4 : 2;
   return ep.ldy % n == 0 && (uintptr_t)ep.y % (n * size) == 0;
 }
 
@@ -630,7 +693,7 @@ hipError_t launch_product(const RunPlan& p, const Side& a, const Side& b, const 
     const int na = (a.tiles + 15) / 16, nb = (b.tiles + 15) / 16;
     auto k = k_mx_tile<FMT, 4, 4, S>;
     lds_limit(k, lds);
-    hipLaunchKernelGGL(k, dim3(na * nb), dim3(256), lds, st, a, b, ep, M, T, ch, qu, na, nb, whole_fours(ep));
+    hipLaunchKernelGGL(k, dim3(na * nb), dim3(256), lds, st, a, b, ep, M, T, ch, qu, na, nb, whole_rows(ep));
   } else {
     hipLaunchKernelGGL(k_mx_simple<FMT>, dim3((a.tiles + 7) / 8, (b.tiles + 1) / 2), dim3(256), 0, st, a, b, ep, M, T, ch, qu);
   }
