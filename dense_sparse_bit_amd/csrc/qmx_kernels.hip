@@ -173,13 +173,6 @@ struct Side {
   int tiles;
 };
 
-__device__ __forceinline__ i32x8_t operand(const uint8_t* p, int lane, bool two) {
-  const u32x4_t a = *(const u32x4_t*)(p + 16 * lane);
-  u32x4_t b = {0, 0, 0, 0};
-  if (two) b = *(const u32x4_t*)(p + 1024 + 16 * lane);
-  return (i32x8_t){(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
-}
-
 // An operand of E4M3 elements in its upper and its lower eight binades.  The scaled MFMA adds E4M3 products with fewer bits
 // than fp32 has below the largest: with all sixteen binades in one operand, sums came out up to 1e-4 of the largest
 // product off (2e-5 of an output's 2-norm); eight at a time add up exactly.
@@ -243,63 +236,139 @@ __device__ __forceinline__ void put4(const EpiArg<true>& ep, int M, int T, int r
   }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows: up to 64 tokens (NB tiles of 16), where the weights' way from memory is
+// the time.  A workgroup takes RT tiles of features over all columns; its waves
+// take the quads (512 columns) in turn, straight from memory into the operands'
+// registers, and all of a quad's loads are on their way at once.  Their sums meet
+// in LDS and are added in the waves' order.
+//
+// ROWS 1, 2: x comes as FP16 or fp32 rows, 16 at most, and a wave quantises its own
+// quads' columns on the way: 8 columns a lane and token, the operands formed by way
+// of LDS.  That saves the launch in front, and its 16 bits a value come from the L2.
+// ---------------------------------------------------------------------------
+template <int FMT, int RT, int NB>
+constexpr int max_waves() {  // 16 have 128 registers each, 8 have 256
+  return (RT + NB * (FMT ? 2 : 1)) * 16 + RT * NB * 4 > 100 ? 8 : 16;
+}
+
 template <int FMT>
-__global__ void __launch_bounds__(256)
-k_mx_simple(Side w, Side x, EpiArg<true> ep, int M, int T, int chunks, int quads) {
-  constexpr int AT = 2, BT = 2;
+struct QuadTokens {  // a wave's quantised quad: tokens' codes, then their exponents
+  static constexpr int stride = FMT ? 528 : 272;  // bytes of a token, 16 of them for the banks
+  static constexpr int exps = 16 * stride;        // [block q][token] dwords
+  static constexpr int bytes = exps + 256;
+};
+
+template <int FMT, int RT, int NB, int ROWS>
+__global__ void __launch_bounds__((64 * max_waves<FMT, RT, NB>()))
+k_mx_stream(Side w, Side x, const void* rows, int64_t ldx, EpiArg<true> ep, int M, int T, int cols, int chunks, int quads) {
+  constexpr int P = FMT ? 2 : 1;
+  extern __shared__ __align__(16) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int a0 = (blockIdx.x * 4 + wave) * AT, b0 = blockIdx.y * BT;
-  if (a0 >= w.tiles) return;
-  floatx4_t acc[AT][BT];
+  const int waves = blockDim.x >> 6, n = lane & 15, kq = lane >> 4;
+  const int a0 = blockIdx.x * RT;
+  const uint8_t *pa[RT], *pb[NB];
+  const int *ea[RT], *eb[NB];
 #pragma unroll
-  for (int i = 0; i < AT; ++i)
-#pragma unroll
-    for (int j = 0; j < BT; ++j) acc[i][j] = (floatx4_t){0, 0, 0, 0};
-  const uint8_t *pa[AT], *pb[BT];
-  const int *ea[AT], *eb[BT];
-#pragma unroll
-  for (int i = 0; i < AT; ++i) {
+  for (int i = 0; i < RT; ++i) {
     const int64_t t = min(a0 + i, w.tiles - 1);
-    pa[i] = w.codes + t * w.tile_bytes;
+    pa[i] = w.codes + t * w.tile_bytes + 16 * lane;
     ea[i] = (const int*)(w.exps + t * quads * 256) + lane;
   }
+  if constexpr (ROWS == 0) {
 #pragma unroll
-  for (int j = 0; j < BT; ++j) {
-    const int64_t t = min(b0 + j, x.tiles - 1);
-    pb[j] = x.codes + t * x.tile_bytes;
-    eb[j] = (const int*)(x.exps + t * quads * 256) + lane;
+    for (int j = 0; j < NB; ++j) {
+      // tokens past the last read the last one's
+      const int t = min(16 * j + n, T - 1);
+      pb[j] = x.codes + (int64_t)(t >> 4) * x.tile_bytes + 256 * kq + 16 * (t & 15);
+      eb[j] = (const int*)(x.exps + (int64_t)(t >> 4) * quads * 256) + 16 * kq + (t & 15);
+    }
   }
-  for (int q = 0; q < quads; ++q) {
-    int sa[AT], sb[BT];
+  floatx4_t acc[RT][NB];
 #pragma unroll
-    for (int i = 0; i < AT; ++i) sa[i] = ea[i][q * 64];
+  for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int j = 0; j < BT; ++j) sb[j] = eb[j][q * 64];
+    for (int j = 0; j < NB; ++j) acc[i][j] = (floatx4_t){0, 0, 0, 0};
+  for (int q = wave; q < quads; q += waves) {
+    u32x4_t A[RT][4];
+    int sa[RT], sb[NB];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        A[i][c] = __builtin_nontemporal_load((const u32x4_t*)(pa[i] + (int64_t)min(4 * q + c, chunks - 1) * 1024));
+      sa[i] = __builtin_nontemporal_load(ea[i] + q * 64);
+    }
+    u32x4_t B[NB][4][P];
+    if constexpr (ROWS == 0) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < P; ++e)
+            B[j][c][e] = *(const u32x4_t*)(pb[j] + (int64_t)min(4 * q + c, chunks - 1) * (1024 * P) + 1024 * e);
+        sb[j] = eb[j][q * 64];
+      }
+    } else {
+      uint8_t* mine = lds + wave * QuadTokens<FMT>::bytes;
+      const int col = 512 * q + 8 * lane;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll 4
+      for (int t = 0; t < T; ++t) {
+        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (col < cols) load8<ROWS == 2>(rows, t * ldx + col, v);
+        uint32_t e[2];
+        const uint32_t byte = mx_quad<FMT>(v, false, e);
+        uint8_t* to = mine + t * QuadTokens<FMT>::stride;
+        if constexpr (FMT == kE2M1) *(uint32_t*)(to + 4 * lane) = e[0];
+        else *(u32x2_t*)(to + 8 * lane) = (u32x2_t){e[0], e[1]};
+        // block b = lane / 4 of the quad: chunk b / 4, block b % 4
+        if ((lane & 3) == 0) mine[QuadTokens<FMT>::exps + 64 * ((lane >> 2) & 3) + 4 * t + (lane >> 4)] = (uint8_t)byte;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      const int t = min(n, T - 1);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int e = 0; e < P; ++e)
+          B[0][c][e] = *(const u32x4_t*)(mine + t * QuadTokens<FMT>::stride + 64 * P * c + 64 * e + 16 * kq);
+      sb[0] = *(const int*)(mine + QuadTokens<FMT>::exps + 64 * kq + 4 * t);
+    }
     auto step = [&](auto J) {
-      constexpr int jj = decltype(J)::value;
-      const int64_t c = 4 * q + jj;
-      if (c >= chunks) return;
-      i32x8_t A[AT];
-      Tokens<FMT> B[BT];
+      constexpr int c = decltype(J)::value;
+      if (4 * q + c >= chunks) return;
 #pragma unroll
-      for (int i = 0; i < AT; ++i) A[i] = operand(pa[i] + c * 1024, lane, false);
+      for (int j = 0; j < NB; ++j) {
+        i32x8_t b = {};
 #pragma unroll
-      for (int j = 0; j < BT; ++j) B[j] = tokens<FMT>(operand(pb[j] + c * (FMT ? 2048 : 1024), lane, FMT == kE4M3));
+        for (int e = 0; e < 4 * P; ++e) b[e] = (int)B[j][c][e / 4][e % 4];
+        const Tokens<FMT> tk = tokens<FMT>(b);
 #pragma unroll
-      for (int i = 0; i < AT; ++i)
-#pragma unroll
-        for (int j = 0; j < BT; ++j) acc[i][j] = mx_mfma<FMT, jj>(A[i], B[j], acc[i][j], sa[i], sb[j]);
+        for (int i = 0; i < RT; ++i) {
+          const i32x8_t a = {(int)A[i][c][0], (int)A[i][c][1], (int)A[i][c][2], (int)A[i][c][3], 0, 0, 0, 0};
+          acc[i][j] = mx_mfma<FMT, c>(a, tk, acc[i][j], sa[i], sb[j]);
+        }
+      }
     };
     step(std::integral_constant<int, 0>{});
     step(std::integral_constant<int, 1>{});
     step(std::integral_constant<int, 2>{});
     step(std::integral_constant<int, 3>{});
   }
+  // [wave][tile][token tile][lane]
+  floatx4_t* sums = (floatx4_t*)lds;
+  if constexpr (ROWS != 0) __syncthreads();  // all waves are done with their tokens
 #pragma unroll
-  for (int i = 0; i < AT; ++i)
+  for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int j = 0; j < BT; ++j)
-      put4(ep, M, T, (a0 + i) * 16 + 4 * (lane >> 4), (b0 + j) * 16 + (lane & 15), acc[i][j]);
+    for (int j = 0; j < NB; ++j) sums[((wave * RT + i) * NB + j) * 64 + lane] = acc[i][j];
+  __syncthreads();
+  for (int at = wave; at < RT * NB; at += waves) {
+    floatx4_t v = sums[at * 64 + lane];
+    for (int k = 1; k < waves; ++k) v += sums[(k * RT * NB + at) * 64 + lane];
+    put4(ep, M, T, (a0 + at / NB) * 16 + 4 * kq, at % NB * 16 + n, v);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -430,7 +499,7 @@ __device__ __forceinline__ void put_tile(const EpiArg<true>& ep, int M, int T, i
 // compiler moves the reads down to their use, and waits for each.
 template <int READS, int MFMAS, int VM>
 __device__ __forceinline__ void spread() {
-  constexpr int per = MFMAS / READS;
+  constexpr int per = MFMAS >= READS ? MFMAS / READS : 1;
 #pragma unroll
   for (int i = 0; i < READS; ++i) {
     __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
@@ -450,13 +519,13 @@ __device__ __forceinline__ void tile_of(int id, int tiles_a, int tiles_b, int& t
   tb = 4 * grp + in - ta * width;
 }
 
-template <int FMT, int AT, int BT, int S>
-__global__ void __launch_bounds__(256, 1)
+template <int FMT, int AT, int BT, int S, int WG>
+__global__ void __launch_bounds__(256, WG)
 k_mx_tile(Side w, Side x, EpiArg<true> ep, int M, int T, int chunks, int quads, int tiles_a, int tiles_b, bool whole) {
   constexpr int P = FMT ? 2 : 1;               // KiB of a token chunk
   constexpr int CA = 4 * AT, CB = 4 * BT * P;  // KiB of a stage
   constexpr int NL = (CA + CB) / 4;            // copies of a wave and stage
-  constexpr int H = 2;                         // the results leave by way of LDS in H parts
+  constexpr int H = BT > 1 ? 2 : 1;            // the results leave by way of LDS in H parts
   extern __shared__ __align__(16) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int ta, tb;
@@ -653,9 +722,14 @@ hipError_t launch_quantize(const Geo& g, void* blocks, const void* x, int type, 
   return hipGetLastError();
 }
 
+// Rows that the stream kernel quantises on the way: every workgroup does so for itself.  4096 x 4096 with E2M1, E4M3, us:
+// 1 row 4.3, 4.9 (a launch in front: 6.5, 7.1), 4 rows 5.4, 6.1 (6.5, 7.2), 8 rows 6.7, 7.6 (6.7, 7.4); 28672 x 8192: 1 row
+// 24.6, 24.8 (27.4, 27.6), 4 rows 28.0, 31.4 (27.5, 27.6).
+bool fused_rows(int T, int x_type) { return x_type != QMX_IN_BLOCKS && T <= 4; }
+
 struct RunPlan {
   Geo gw, gx;
-  size_t x_bytes, bytes;
+  size_t bytes;  // workspace: x in blocks
 };
 
 int run_plan(const qmx_shape* w, const qmx_input* x, const qgemv_epilogue* e, RunPlan& p) {
@@ -668,8 +742,7 @@ int run_plan(const qmx_shape* w, const qmx_input* x, const qgemv_epilogue* e, Ru
   if (x->x_type != QMX_IN_BLOCKS && x->x_type != QGEMV_F16 && x->x_type != QGEMV_F32) return QGEMV_ERR_UNSUPPORTED;
   p.gw = geo(w->rows, w->cols, w->format);
   p.gx = geo(x->rows, w->cols, x->format);
-  p.x_bytes = x->x_type == QMX_IN_BLOCKS ? 0 : (size_t)p.gx.bytes;
-  p.bytes = p.x_bytes;
+  p.bytes = x->x_type == QMX_IN_BLOCKS || fused_rows(x->rows, x->x_type) ? 0 : (size_t)p.gx.bytes;
   return QGEMV_OK;
 }
 
@@ -684,18 +757,99 @@ bool whole_rows(const EpiArg<true>& ep) {
   return ep.ldy % n == 0 && (uintptr_t)ep.y % (n * size) == 0;
 }
 
+template <int FMT, int AT, int BT, int S, int WG>
+void launch_tile(const RunPlan& p, const Side& a, const Side& b, const EpiArg<true>& ep, hipStream_t st) {
+  constexpr int ring = S * (4 * AT + 4 * BT * (FMT ? 2 : 1)) * 1024, out = 4 * (BT > 1 ? 16 * BT : 32) * (32 * AT + 4) * 4;
+  constexpr int lds = ring > out ? ring : out;
+  const int na = (a.tiles + 4 * AT - 1) / (4 * AT), nb = (b.tiles + 4 * BT - 1) / (4 * BT);
+  auto k = k_mx_tile<FMT, AT, BT, S, WG>;
+  lds_limit(k, lds);
+  hipLaunchKernelGGL(k, dim3(na * nb), dim3(256), lds, st, a, b, ep, p.gw.rows, p.gx.rows, p.gw.chunks, p.gw.quads, na, nb,
+                     whole_rows(ep));
+}
+
+template <int FMT, int RT, int NB, int ROWS>
+void launch_stream(const RunPlan& p, const Side& a, const Side& b, const EpiArg<true>& ep, const qmx_input* x, hipStream_t st) {
+  // as many waves as share the quads evenly
+  constexpr int most = max_waves<FMT, RT, NB>();
+  const int rounds = (p.gw.quads + most - 1) / most, waves = (p.gw.quads + rounds - 1) / rounds;
+  const int sums = waves * RT * NB * 1024, tokens = ROWS ? waves * QuadTokens<FMT>::bytes : 0;
+  const int lds = sums > tokens ? sums : tokens;
+  auto k = k_mx_stream<FMT, RT, NB, ROWS>;
+  lds_limit(k, lds);
+  hipLaunchKernelGGL(k, dim3((a.tiles + RT - 1) / RT), dim3(64 * waves), lds, st, a, b, x->data, x->ldx, ep, p.gw.rows,
+                     p.gx.rows, p.gw.cols, p.gw.chunks, p.gw.quads);
+}
+
+// Tiles of features a workgroup takes: as many as leave work for all CUs, since tokens are read once for all of them.
+// 256 | 1376 | 1792 tiles of 4096 | 4096 | 8192 columns, E2M1, 16 rows: 1 tile 5.2 | 14.0 | 31.3 us, 2 tiles
+// 5.7 | 12.1 | 28.1, 4 tiles 6.3 | 13.3 | 26.9.
+template <int FMT, int NB, int ROWS>
+void stream_by_tiles(const RunPlan& p, const Side& a, const Side& b, const EpiArg<true>& ep, const qmx_input* x,
+                     hipStream_t st) {
+  if constexpr (NB == 1) {
+    if (a.tiles >= 1536) return launch_stream<FMT, 4, NB, ROWS>(p, a, b, ep, x, st);
+  }
+  if (a.tiles >= 512) launch_stream<FMT, 2, NB, ROWS>(p, a, b, ep, x, st);
+  else launch_stream<FMT, 1, NB, ROWS>(p, a, b, ep, x, st);
+}
+
+// Whether the tile kernel's copies through LDS are the faster way for up to 64 rows: it takes about the same time for any
+// number of features that fill the CUs once, the stream kernel time by the weight.  E2M1, us, stream | tile:
+//   1 row     22016 x 4096: 10.4 | 11.8   28672 x 8192: 26.4 | 21.7
+//   32 rows   4096 x 11008:  8.7 | 15.8   22016 x 4096: 14.1 | 12.3   28672 x 8192: 28.5 | 22.2
+//   64 rows   4096 x 11008: 11.2 | 15.8   22016 x 4096: 21.2 | 12.4   28672 x 8192: 34.8 | 22.5
+// E4M3 rows cost the tile kernel two MFMAs of twice the time:
+//   32 rows   22016 x 4096: 19.1 | 19.8   28672 x 8192: 34.1 | 33.2
+//   64 rows   4096 x 11008: 18.6 | 36.8   22016 x 4096: 30.1 | 19.9   28672 x 8192: 61.2 | 33.5
 template <int FMT>
-hipError_t launch_product(const RunPlan& p, const Side& a, const Side& b, const EpiArg<true>& ep, hipStream_t st) {
-  const int M = p.gw.rows, T = p.gx.rows, ch = p.gw.chunks, qu = p.gw.quads;
-  if (T >= 256) {
-    constexpr int S = FMT ? 3 : 4, ring = S * (16 + 16 * (FMT ? 2 : 1)) * 1024, out = 4 * 64 * (128 + 4) * 4;
-    constexpr int lds = ring > out ? ring : out;
-    const int na = (a.tiles + 15) / 16, nb = (b.tiles + 15) / 16;
-    auto k = k_mx_tile<FMT, 4, 4, S>;
-    lds_limit(k, lds);
-    hipLaunchKernelGGL(k, dim3(na * nb), dim3(256), lds, st, a, b, ep, M, T, ch, qu, na, nb, whole_rows(ep));
+bool tiles_for_few(int M, int T) {
+  if (FMT == kE4M3) return T > 32 && M >= 12288;
+  return M >= (T > 32 ? 8192 : T > 16 ? 16384 : 24576);
+}
+
+// The tile shape of the least time by a model: so much for a call, and for a chunk, the time that a workgroup takes
+// that has a CU for itself, or its share of a full CU times the workgroups of a CU.  The times, in us, are fits to products
+// of 4096 x 4096 to 28672 x 8192 with 64 to 8192 rows, which the model meets within some 10 %.
+struct TileCost {
+  int features, tokens;
+  float call, alone, full;
+};
+template <int FMT>
+int best_tile(int M, int T, int chunks) {
+  static const TileCost e2m1[] = {{64, 64, 4.6f, 0.13f, 0.117f}, {128, 64, 5.2f, 0.185f, 0.193f},
+                                  {128, 128, 6.3f, 0.217f, 0.286f}, {128, 256, 8.7f, 0.37f, 0.525f}};
+  static const TileCost e4m3[] = {{64, 64, 5.3f, 0.37f, 0.26f}, {128, 64, 5.7f, 0.4f, 0.38f}, {256, 128, 9.3f, 1.1f, 1.2f}};
+  const TileCost* c = FMT ? e4m3 : e2m1;
+  int best = 0;
+  float least = 0.f;
+  for (int i = 0; i < (FMT ? 3 : 4); ++i) {
+    const int64_t n = (int64_t)((M + c[i].features - 1) / c[i].features) * ((T + c[i].tokens - 1) / c[i].tokens);
+    const float of_cu = (float)((n + 255) / 256) * c[i].full;
+    const float t = c[i].call + chunks * (of_cu > c[i].alone ? of_cu : c[i].alone);
+    if (i == 0 || t < least) least = t, best = i;
+  }
+  return best;
+}
+
+template <int FMT>
+hipError_t launch_product(const RunPlan& p, const Side& a, const Side& b, const EpiArg<true>& ep, const qmx_input* x,
+                          hipStream_t st) {
+  const int M = p.gw.rows, T = p.gx.rows;
+  if (fused_rows(T, x->x_type)) {
+    if (x->x_type == QGEMV_F32) stream_by_tiles<FMT, 1, 2>(p, a, b, ep, x, st);
+    else stream_by_tiles<FMT, 1, 1>(p, a, b, ep, x, st);
+  } else if (T <= 64 && !tiles_for_few<FMT>(M, T)) {
+    if (T <= 16) stream_by_tiles<FMT, 1, 0>(p, a, b, ep, x, st);
+    else if (T <= 32) stream_by_tiles<FMT, 2, 0>(p, a, b, ep, x, st);
+    else launch_stream<FMT, 1, 4, 0>(p, a, b, ep, x, st);
   } else {
-    hipLaunchKernelGGL(k_mx_simple<FMT>, dim3((a.tiles + 7) / 8, (b.tiles + 1) / 2), dim3(256), 0, st, a, b, ep, M, T, ch, qu);
+    const int i = T <= 64 ? 1 : best_tile<FMT>(M, T, p.gw.chunks);
+    if (i == 0) launch_tile<FMT, 1, 1, FMT ? 5 : 8, 2>(p, a, b, ep, st);
+    else if (i == 1) launch_tile<FMT, 2, 1, FMT ? 4 : 5, 2>(p, a, b, ep, st);
+    else if constexpr (FMT == kE4M3) launch_tile<FMT, 4, 2, 2, 2>(p, a, b, ep, st);
+    else if (i == 2) launch_tile<FMT, 2, 2, 4, 2>(p, a, b, ep, st);
+    else launch_tile<FMT, 2, 4, 3, 2>(p, a, b, ep, st);
   }
   return hipGetLastError();
 }
@@ -788,12 +942,12 @@ int qmx_run(const qmx_shape* w, const void* w_blocks, const qmx_input* x, void* 
   if (p.bytes > 0 && (!ws || (uintptr_t)ws % 256)) return QGEMV_ERR_INVALID_ARG;
   if (ws_bytes < p.bytes) return QGEMV_ERR_SIZE;
   const hipStream_t s = (hipStream_t)stream;
-  if (x->x_type != QMX_IN_BLOCKS) {
+  if (p.bytes > 0) {
     const hipError_t er = launch_quantize(p.gx, ws, xb, x->x_type, x->ldx, 0, s);
     if (er != hipSuccess) return hip_status(er);
     xb = ws;
   }
   const Side a = side(w_blocks, p.gw), b = side(xb, p.gx);
-  return hip_status(p.gx.fmt == QMX_E2M1 ? launch_product<kE2M1>(p, a, b, ep, s) : launch_product<kE4M3>(p, a, b, ep, s));
+  return hip_status(p.gx.fmt == QMX_E2M1 ? launch_product<kE2M1>(p, a, b, ep, x, s) : launch_product<kE4M3>(p, a, b, ep, x, s));
 }
 }  // extern "C"
