@@ -742,13 +742,10 @@ int run_plan(const qmx_shape* w, const qmx_input* x, const qgemv_epilogue* e, Ru
   if (x->x_type != QMX_IN_BLOCKS && x->x_type != QGEMV_F16 && x->x_type != QGEMV_F32) return QGEMV_ERR_UNSUPPORTED;
   p.gw = geo(w->rows, w->cols, w->format);
   p.gx = geo(x->rows, w->cols, x->format);
+  // the smallest tiles' workgroups, fewer than 2^32 threads a launch
+  if ((int64_t)((p.gw.tiles + 3) / 4) * ((p.gx.tiles + 3) / 4) >= 1 << 24) return QGEMV_ERR_UNSUPPORTED;
   p.bytes = x->x_type == QMX_IN_BLOCKS || fused_rows(x->rows, x->x_type) ? 0 : (size_t)p.gx.bytes;
   return QGEMV_OK;
-}
-
-template <class F>
-void lds_limit(F k, int bytes) {
-  (void)hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
 // Whether a lane's eight outputs (four when gated) can be stored together, 16 bytes or the whole at a time.
@@ -757,41 +754,48 @@ bool whole_rows(const EpiArg<true>& ep) {
   return ep.ldy % n == 0 && (uintptr_t)ep.y % (n * size) == 0;
 }
 
+constexpr int kLdsBytes = 160 * 1024;
+
 template <int FMT, int AT, int BT, int S, int WG>
-void launch_tile(const RunPlan& p, const Side& a, const Side& b, const EpiArg<true>& ep, hipStream_t st) {
+hipError_t launch_tile(const RunPlan& p, const Side& a, const Side& b, const EpiArg<true>& ep, hipStream_t st) {
   constexpr int ring = S * (4 * AT + 4 * BT * (FMT ? 2 : 1)) * 1024, out = 4 * (BT > 1 ? 16 * BT : 32) * (32 * AT + 4) * 4;
   constexpr int lds = ring > out ? ring : out;
   const int na = (a.tiles + 4 * AT - 1) / (4 * AT), nb = (b.tiles + 4 * BT - 1) / (4 * BT);
   auto k = k_mx_tile<FMT, AT, BT, S, WG>;
-  lds_limit(k, lds);
+  // once per instantiation (thread-safe static initialisation)
+  static const hipError_t attr = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (attr != hipSuccess) return attr;
   hipLaunchKernelGGL(k, dim3(na * nb), dim3(256), lds, st, a, b, ep, p.gw.rows, p.gx.rows, p.gw.chunks, p.gw.quads, na, nb,
                      whole_rows(ep));
+  return hipGetLastError();
 }
 
 template <int FMT, int RT, int NB, int ROWS>
-void launch_stream(const RunPlan& p, const Side& a, const Side& b, const EpiArg<true>& ep, const qmx_input* x, hipStream_t st) {
+hipError_t launch_stream(const RunPlan& p, const Side& a, const Side& b, const EpiArg<true>& ep, const qmx_input* x, hipStream_t st) {
   // as many waves as share the quads evenly
   constexpr int most = max_waves<FMT, RT, NB>();
   const int rounds = (p.gw.quads + most - 1) / most, waves = (p.gw.quads + rounds - 1) / rounds;
   const int sums = waves * RT * NB * 1024, tokens = ROWS ? waves * QuadTokens<FMT>::bytes : 0;
   const int lds = sums > tokens ? sums : tokens;
   auto k = k_mx_stream<FMT, RT, NB, ROWS>;
-  lds_limit(k, lds);
+  static const hipError_t attr = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, kLdsBytes);
+  if (attr != hipSuccess) return attr;
   hipLaunchKernelGGL(k, dim3((a.tiles + RT - 1) / RT), dim3(64 * waves), lds, st, a, b, x->data, x->ldx, ep, p.gw.rows,
                      p.gx.rows, p.gw.cols, p.gw.chunks, p.gw.quads);
+  return hipGetLastError();
 }
 
 // Tiles of features a workgroup takes: as many as leave work for all CUs, since tokens are read once for all of them.
 // 256 | 1376 | 1792 tiles of 4096 | 4096 | 8192 columns, E2M1, 16 rows: 1 tile 5.2 | 14.0 | 31.3 us, 2 tiles
 // 5.7 | 12.1 | 28.1, 4 tiles 6.3 | 13.3 | 26.9.
 template <int FMT, int NB, int ROWS>
-void stream_by_tiles(const RunPlan& p, const Side& a, const Side& b, const EpiArg<true>& ep, const qmx_input* x,
-                     hipStream_t st) {
+hipError_t stream_by_tiles(const RunPlan& p, const Side& a, const Side& b, const EpiArg<true>& ep, const qmx_input* x,
+                           hipStream_t st) {
   if constexpr (NB == 1) {
     if (a.tiles >= 1536) return launch_stream<FMT, 4, NB, ROWS>(p, a, b, ep, x, st);
   }
-  if (a.tiles >= 512) launch_stream<FMT, 2, NB, ROWS>(p, a, b, ep, x, st);
-  else launch_stream<FMT, 1, NB, ROWS>(p, a, b, ep, x, st);
+  if (a.tiles >= 512) return launch_stream<FMT, 2, NB, ROWS>(p, a, b, ep, x, st);
+  return launch_stream<FMT, 1, NB, ROWS>(p, a, b, ep, x, st);
 }
 
 // Whether the tile kernel's copies through LDS are the faster way for up to 64 rows: it takes about the same time for any
@@ -836,22 +840,22 @@ template <int FMT>
 hipError_t launch_product(const RunPlan& p, const Side& a, const Side& b, const EpiArg<true>& ep, const qmx_input* x,
                           hipStream_t st) {
   const int M = p.gw.rows, T = p.gx.rows;
-  if (fused_rows(T, x->x_type)) {
-    if (x->x_type == QGEMV_F32) stream_by_tiles<FMT, 1, 2>(p, a, b, ep, x, st);
-    else stream_by_tiles<FMT, 1, 1>(p, a, b, ep, x, st);
-  } else if (T <= 64 && !tiles_for_few<FMT>(M, T)) {
-    if (T <= 16) stream_by_tiles<FMT, 1, 0>(p, a, b, ep, x, st);
-    else if (T <= 32) stream_by_tiles<FMT, 2, 0>(p, a, b, ep, x, st);
-    else launch_stream<FMT, 1, 4, 0>(p, a, b, ep, x, st);
-  } else {
-    const int i = T <= 64 ? 1 : best_tile<FMT>(M, T, p.gw.chunks);
-    if (i == 0) launch_tile<FMT, 1, 1, FMT ? 5 : 8, 2>(p, a, b, ep, st);
-    else if (i == 1) launch_tile<FMT, 2, 1, FMT ? 4 : 5, 2>(p, a, b, ep, st);
-    else if constexpr (FMT == kE4M3) launch_tile<FMT, 4, 2, 2, 2>(p, a, b, ep, st);
-    else if (i == 2) launch_tile<FMT, 2, 2, 4, 2>(p, a, b, ep, st);
-    else launch_tile<FMT, 2, 4, 3, 2>(p, a, b, ep, st);
+  if (fused_rows(T, x->x_type))
+    return x->x_type == QGEMV_F32 ? stream_by_tiles<FMT, 1, 2>(p, a, b, ep, x, st) : stream_by_tiles<FMT, 1, 1>(p, a, b, ep, x, st);
+  if (T <= 64 && !tiles_for_few<FMT>(M, T)) {
+    if (T <= 16) return stream_by_tiles<FMT, 1, 0>(p, a, b, ep, x, st);
+    if (T <= 32) return stream_by_tiles<FMT, 2, 0>(p, a, b, ep, x, st);
+    return launch_stream<FMT, 1, 4, 0>(p, a, b, ep, x, st);
   }
-  return hipGetLastError();
+  const int i = T <= 64 ? 1 : best_tile<FMT>(M, T, p.gw.chunks);
+  if (i == 0) return launch_tile<FMT, 1, 1, FMT ? 5 : 8, 2>(p, a, b, ep, st);
+  if (i == 1) return launch_tile<FMT, 2, 1, FMT ? 4 : 5, 2>(p, a, b, ep, st);
+  if constexpr (FMT == kE4M3) {
+    return launch_tile<FMT, 4, 2, 2, 2>(p, a, b, ep, st);
+  } else {
+    if (i == 2) return launch_tile<FMT, 2, 2, 4, 2>(p, a, b, ep, st);
+    return launch_tile<FMT, 2, 4, 3, 2>(p, a, b, ep, st);
+  }
 }
 
 }  // namespace
