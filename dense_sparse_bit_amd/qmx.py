@@ -188,8 +188,7 @@ class QMx:
         if act not in ACT:
             raise ValueError(f"act must be one of {sorted(ACT)}")
         mo = self.M // 2 if gated else self.M
-        e = Epilogue()
-        e.act, e.gated = ACT[act], bool(gated)
+        e = Epilogue(ACT[act], bool(gated))
         if bias is not None:
             f32 = bias.dtype == torch.float32
             if (not f32 and bias.dtype != torch.float16) or bias.shape != (self.M,) or not bias.is_contiguous() or (
@@ -209,13 +208,15 @@ class QMx:
             if dtype is not None and dtype != out.dtype:
                 raise ValueError("dtype is not that of out")
             y, e.y_type, e.ldy = QGemv._output_rows(out, T, mo, at, "out")
-        n = ctypes.c_size_t(0)
-        L = lib()
-        st = L.qmx_run_ws(self.w._shape, xi, e, n)
-        if st == 0:
-            # its own for every call: calls on other streams, and captured ones, never share it
-            ws = self.w.data.new_empty(n.value) if n.value else None
-            st = L.qmx_run(self.w._shape, self.w.data.data_ptr(), xi, y, e, ws.data_ptr() if n.value else None, n.value, s)
+        L, ws, size = lib(), None, 0
+        if not isinstance(x, MxRows):  # blocks need none
+            n = ctypes.c_size_t(0)
+            _check(L.qmx_run_ws(self.w._shape, xi, e, n), "qmx_run_ws")
+            size = n.value
+            if size:
+                # its own for every call: calls on other streams, and captured ones, never share it
+                ws = self.w.data.new_empty(size)
+        st = L.qmx_run(self.w._shape, self.w.data.data_ptr(), xi, y, e, ws.data_ptr() if size else None, size, s)
         if st != 0:
             raise QgemvError(st, "qmx_run")
         return out

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
@@ -29,6 +30,10 @@ class Args(ctypes.Structure):
                                                                   "pre_bias", "h_out", "out")]
 
 
+# an Args' bytes from plain numbers: building the ctypes structure of a call takes 3 us, this 0.6
+_args = struct.Struct("@iiiff" + 9 * "Piq").pack
+_NONE = (0, 0, 0)
+
 _lib = None
 
 
@@ -37,27 +42,28 @@ def lib() -> ctypes.CDLL:
     global _lib
     if _lib is None:
         L = _qgemv_lib()
-        L.qnorm_run.argtypes = [ctypes.POINTER(Args), ctypes.c_void_p]
+        L.qnorm_run.argtypes = [ctypes.c_void_p, ctypes.c_void_p]  # an Args by reference, or its bytes
         L.qnorm_run.restype = ctypes.c_int
         _lib = L
     return _lib
 
 
 def _matrix(t, T, N, at, what):
-    dt = t.dtype
-    if (dt != torch.float16 and dt != torch.float32) or t.shape != (T, N) or t.get_device() != at:
+    """(pointer, is fp32, row stride) of a [T, N] tensor with contiguous rows; a stride that does not matter is 0."""
+    f32 = t.dtype is torch.float32
+    if (not f32 and t.dtype is not torch.float16) or t.shape != (T, N) or t.get_device() != at:
         raise ValueError(f"{what} must be an FP16 or fp32 [T, N] tensor on the same device")
     ld, one = t.stride()
     if one != 1:
         raise ValueError(f"{what} must have contiguous rows")
-    return Rows(t.data_ptr(), dt == torch.float32, ld if T > 1 else 0)
+    return t.data_ptr(), f32, ld if T > 1 else 0
 
 
 def _vector(t, N, at, what):
-    dt = t.dtype
-    if (dt != torch.float16 and dt != torch.float32) or t.shape != (N,) or not t.is_contiguous() or t.get_device() != at:
+    f32 = t.dtype is torch.float32
+    if (not f32 and t.dtype is not torch.float16) or t.shape != (N,) or t.stride(0) != 1 or t.get_device() != at:
         raise ValueError(f"{what} must be a contiguous FP16 or fp32 [N] tensor on the same device")
-    return Rows(t.data_ptr(), dt == torch.float32, 0)
+    return t.data_ptr(), f32, 0
 
 
 def norm(y, h=None, post=None, post_bias=None, gate=None, scale=1.0, pre=None, pre_bias=None, kind="rms", eps=1e-6,
@@ -92,45 +98,46 @@ def norm(y, h=None, post=None, post_bias=None, gate=None, scale=1.0, pre=None, p
     T, N = lead.shape
     if max(T, N) > 2**31 - 1:
         raise ValueError("counts are 32-bit")
-    a = Args(T, N, KIND[kind], eps, scale)
-    if y is not None:
-        a.y = _matrix(y, T, N, at, "y")
-    if h is not None:
-        a.h = _matrix(h, T, N, at, "h")
-    if gate is not None:
-        if y is None:
-            raise ValueError("a gate needs y")
-        a.gate = _vector(gate, N, at, "gate") if gate.dim() == 1 else _matrix(gate, T, N, at, "gate")
-    for name, v in (("post", post), ("post_bias", post_bias), ("pre", pre), ("pre_bias", pre_bias)):
-        if v is not None:
-            setattr(a, name, _vector(v, N, at, name))
-    if (post is None and post_bias is not None) or (pre is None and pre_bias is not None) or (y is None and post is not None):
-        raise ValueError("a bias needs its weight, and post needs y")
-    if h_out is None and keep_h:
-        h_out = torch.empty_like(h if h is not None else y, memory_format=torch.contiguous_format)
+    if (post is None and post_bias is not None) or (pre is None and pre_bias is not None):
+        raise ValueError("a bias needs its weight")
+    if y is None and (gate is not None or post is not None):
+        raise ValueError("gate and post need y")
+    a_y = _NONE if y is None else _matrix(y, T, N, at, "y")
+    a_h = _NONE if h is None else _matrix(h, T, N, at, "h")
+    a_gate = _NONE if gate is None else _vector(gate, N, at, "gate") if gate.dim() == 1 else _matrix(gate, T, N, at, "gate")
+    a_post = _NONE if post is None else _vector(post, N, at, "post")
+    a_pb = _NONE if post_bias is None else _vector(post_bias, N, at, "post_bias")
+    a_pre = _NONE if pre is None else _vector(pre, N, at, "pre")
+    a_prb = _NONE if pre_bias is None else _vector(pre_bias, N, at, "pre_bias")
+    a_ho = a_out = _NONE
     if h_out is not None:
-        a.h_out = _matrix(h_out, T, N, at, "h_out")
+        a_ho = _matrix(h_out, T, N, at, "h_out")
+    elif keep_h:
+        like = y if h is None else h
+        h_out = like.new_empty(T, N)
+        a_ho = (h_out.data_ptr(), like.dtype is torch.float32, N)
     if pre is None:
         if out is not None:
             raise ValueError("out needs pre")
         if h_out is None:
             raise ValueError("there is nothing to write")
+    elif out is None and out_type in _TYPE:
+        out = lead.new_empty(T, N, dtype=_TYPE[out_type])
+        a_out = (out.data_ptr(), out_type == "fp32", N)
     else:
         if out is None:
-            if out_type in FORMAT:
-                out = MxRows(T, N, out_type, lead.device)
-            elif out_type in _TYPE:
-                out = lead.new_empty(T, N, dtype=_TYPE[out_type])
-            else:
+            if out_type not in FORMAT:
                 raise ValueError(f"out_type must be one of {sorted([*_TYPE, *FORMAT])}")
+            out = MxRows(T, N, out_type, lead.device)
         if isinstance(out, MxRows):
-            if (out.rows, out.cols) != (T, N) or out.data.get_device() != at:
+            if out.rows != T or out.cols != N or out.data.get_device() != at:
                 raise ValueError("out must be [T, N] on the same device")
-            a.out = Rows(out.data.data_ptr(), _BLOCKS + FORMAT[out.fmt], 0)
+            a_out = (out.data.data_ptr(), _BLOCKS + FORMAT[out.fmt], 0)
         else:
-            a.out = _matrix(out, T, N, at, "out")
+            a_out = _matrix(out, T, N, at, "out")
     if T > 0:
-        st = lib().qnorm_run(a, s)
+        st = lib().qnorm_run(_args(T, N, KIND[kind], eps, scale, *a_y, *a_h, *a_gate, *a_post, *a_pb, *a_pre, *a_prb, *a_ho,
+                                   *a_out), s)
         if st != 0:
             raise QgemvError(st, "qnorm_run")
     return h_out, out

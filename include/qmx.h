@@ -81,7 +81,7 @@ typedef struct {
   int64_t ldx;
 } qmx_input;
 
-/* Workspace of qmx_run for these counts (x->data is not looked at).  Host only.  Errors: as qmx_run. */
+/* Workspace of qmx_run for these counts (x->data is not looked at); 0 for x in blocks.  Host only.  Errors: as qmx_run. */
 int qmx_run_ws(const qmx_shape* w, const qmx_input* x, const qgemv_epilogue* e, size_t* bytes);
 
 /*

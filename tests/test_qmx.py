@@ -110,11 +110,13 @@ def test_calls_refused_on_the_host():
     assert run(w=qmx.Shape(5, 64, 0), gated=1) == -3 and run(ldy=5) == -1 and run(residual=4096, ldr=5) == -1
     assert run(residual=4097) == -1 and run(bias=4097) == -1
     assert run(x_type=0, ldx=64, data=4104) == -1 and run(x_type=0, ldx=68) == -1
-    assert run(x_type=0, ldx=64, ws=None) == -1 and run(x_type=0, ldx=64, ws=4096 + 32) == -1
-    assert run(x_type=0, ldx=64, n=64) == -5
+    few = dict(rows=17, x_type=0, ldx=64)
+    assert run(**few, ws=None) == -1 and run(**few, ws=4096 + 32) == -1 and run(**few, n=64) == -5
+    assert run(w=qmx.Shape(1 << 20, 64, 0), rows=1 << 17, ldy=1 << 20) == -3  # past a launch
     n = ctypes.c_size_t(0)
-    x = qmx.Input(None, 3, 0, 0, 64)
+    x = qmx.Input(None, 17, 0, 0, 64)
     assert L.qmx_run_ws(qmx.Shape(6, 64, 0), x, qgemv.Epilogue(), n) == 0 and n.value > 0
+    assert L.qmx_run_ws(qmx.Shape(6, 64, 0), qmx.Input(None, 17, 0, -1, 0), qgemv.Epilogue(), n) == 0 and n.value == 0
     assert L.qmx_run_ws(qmx.Shape(6, 64, 0), x, qgemv.Epilogue(), None) == -1
     assert L.qmx_run_ws(qmx.Shape(6, 64, 0), None, qgemv.Epilogue(), n) == -1
     assert run(rows=0, data=None, y=None, ws=None, n=0) == 0  # no rows: nothing is done

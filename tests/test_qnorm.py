@@ -57,7 +57,7 @@ R = qnorm.Rows
     (-1, dict(out=R(4096 + 128, 16, 0))), (-3, dict(cols=40, out=R(4096, 17, 0))), (0, dict(rows=0))])
 def test_refused(want, kw):
     """Refused before a launch; the pointers are never followed."""
-    assert qnorm.lib().qnorm_run(args(**kw), None) == want
+    assert qnorm.lib().qnorm_run(ctypes.byref(args(**kw)), None) == want
 
 
 def test_null():
