@@ -633,8 +633,9 @@ k_mx_tile(Side w, Side x, EpiArg<true> ep, int M, int T, int chunks, int quads, 
     multiply(I0{}, J);
     spread<AT + BT * P, AT * BT * P, 0>();
     __builtin_amdgcn_sched_barrier(0);
-    // The next chunk has landed; on the way since then are S - 2 stages, and the next exponents.
-    wait_vm<(S - 2) * NL + (jj >= 1 && jj < S ? 2 * (AT + BT) : 0)>();
+    // The next chunk has landed: of what was issued behind it, S - 2 stages may be on the way, and the next exponents where they
+    // were issued in a later step than it.  (In the same step, jj == S - 1, their order is the compiler's.)
+    wait_vm<(S - 2) * NL + (jj >= 1 && jj < S - 1 ? 2 * (AT + BT) : 0)>();
     wait_lgkm();  // the chunk's operands are in registers, its place is free for all behind the barrier
     wave_barrier();
     stage(c + S);

@@ -284,6 +284,29 @@ def test_product_of_wide_ranges(torch, T, M, K, fmt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,M,K", [(64, 24576, 1024), (300, 4096, 4096), (1000, 8192, 2048), (1030, 4096, 8192), (2050, 22016, 1184),
+                                   (4000, 8192, 4096), (8192, 14336, 512)])
+def test_product_of_many_workgroups(torch, T, M, K, fmt):
+    """Every output of products that fill the card several times over, three times in a row: the copies through LDS have all
+    landed when they are read."""
+    rng = np.random.default_rng(T + K)
+    say(f"[gpu] product T {T} M {M} K {K} {fmt}")
+    wc, we = torch.randint(0, 256, (M, K // 2), device="cuda", dtype=torch.uint8), torch.randint(
+        118, 123, (M, K // 32), device="cuda", dtype=torch.uint8)
+    w = qmx.MxRows.pack(wc, we)
+    plan, x = qmx.QMx(w), qmx.quantize(torch.randn((T, K), device="cuda") * float(rng.uniform(0.5, 2)), fmt)
+    xv, wv = x.values().double(), w.values().double()
+    want = xv @ wv.t()
+    tol = ((128 + K / 128 + 16) * 2.0 ** -24 + 2.0 ** -24) * (xv.abs() @ wv.abs().t()) + 2.0 ** -126  # and the output's rounding
+    ys = [plan.run(x, dtype=torch.float32) for _ in range(3)]
+    for y in ys:
+        worst = ((y.double() - want).abs() / tol).max().item()
+        assert worst <= 1, f"worst |dy| / tol = {worst:.3f}"
+        assert torch.equal(y, ys[0])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("T,M,K", [(1, 96, 256), (16, 130, 512), (19, 70, 352), (70, 522, 1024), (260, 514, 640)])
