@@ -151,7 +151,11 @@ k_qnorm(NormArgs a) {
         if constexpr (LAYER) x[j][i] = first + j * step < a.cols ? x[j][i] - mean : 0.f;
         sq = __builtin_fmaf(x[j][i], x[j][i], sq);
       }
-    const float r = 1.f / sqrtf(row_sum<W>(sq, s_sum, turn, wave) * a.inv_n + a.eps);
+    // 1 / sqrt(m) in two parts: what the root and the reciprocal round off is the same for the whole row
+    const float m = __builtin_fmaf(row_sum<W>(sq, s_sum, turn, wave), a.inv_n, a.eps);
+    const float s = sqrtf(m), r = 1.f / s;
+    const float off = __builtin_fmaf(-r, s, 1.f) - 0.5f * (r * r) * __builtin_fmaf(-s, s, m);
+    const float lo = s > 0.f && s < INFINITY ? r * off : 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int col = first + j * step;
@@ -162,7 +166,7 @@ k_qnorm(NormArgs a) {
       if (bias.data) of_raw8(bias, b8[j], b);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float t = x[j][i] * r;
+        const float t = __builtin_fmaf(x[j][i], lo, x[j][i] * r);
         x[j][i] = bias.data ? __builtin_fmaf(t, w[i], b[i]) : t * w[i];
       }
     }
