@@ -815,25 +815,28 @@ bool tiles_for_few(int M, int T) {
   return M >= (T > 32 ? 8192 : T > 16 ? 16384 : 24576);
 }
 
-// The tile shape of the least time by a model: so much for a call, and for a chunk, the time that a workgroup takes
-// that has a CU for itself, or its share of a full CU times the workgroups of a CU.  The times, in us, are fits to products
-// of 4096 x 4096 to 28672 x 8192 with 64 to 8192 rows, which the model meets within some 10 %.
+// The tile shape of the least time by a model: so much for a call, and for a workgroup `end` and `chunk` a chunk where two
+// share a CU, `alone` a chunk at least where one has it for itself; a quarter of a workgroup's time more for the last ones
+// where there are several to a CU.  In us, fits to products of 4096 x 4096 to 28672 x 8192 with 128 to 2048 rows,
+// which the model meets within 10 %.
 struct TileCost {
   int features, tokens;
-  float call, alone, full;
+  float call, alone, chunk, end;
 };
 template <int FMT>
 int best_tile(int M, int T, int chunks) {
-  static const TileCost e2m1[] = {{64, 64, 4.6f, 0.13f, 0.117f}, {128, 64, 5.2f, 0.185f, 0.193f},
-                                  {128, 128, 6.3f, 0.217f, 0.286f}, {128, 256, 8.7f, 0.37f, 0.525f}};
-  static const TileCost e4m3[] = {{64, 64, 5.3f, 0.37f, 0.26f}, {128, 64, 5.7f, 0.4f, 0.38f}, {256, 128, 9.3f, 1.1f, 1.2f}};
+  static const TileCost e2m1[] = {{64, 64, 4.6f, 0.13f, 0.096f, 1.2f}, {128, 64, 5.2f, 0.185f, 0.169f, 1.4f},
+                                  {128, 128, 6.3f, 0.217f, 0.244f, 2.2f}, {128, 256, 8.7f, 0.37f, 0.443f, 4.2f}};
+  static const TileCost e4m3[] = {{64, 64, 5.3f, 0.37f, 0.243f, 1.2f}, {128, 64, 5.7f, 0.4f, 0.345f, 2.3f},
+                                  {256, 128, 9.3f, 1.1f, 1.07f, 7.6f}};
   const TileCost* c = FMT ? e4m3 : e2m1;
   int best = 0;
   float least = 0.f;
   for (int i = 0; i < (FMT ? 3 : 4); ++i) {
     const int64_t n = (int64_t)((M + c[i].features - 1) / c[i].features) * ((T + c[i].tokens - 1) / c[i].tokens);
-    const float of_cu = (float)((n + 255) / 256) * c[i].full;
-    const float t = c[i].call + chunks * (of_cu > c[i].alone ? of_cu : c[i].alone);
+    const float of_cu = n <= 256 ? 1.f : (float)n / 256.f + 0.25f;
+    const float share = of_cu * (chunks * c[i].chunk + c[i].end), alone = chunks * c[i].alone;
+    const float t = c[i].call + (share > alone ? share : alone);
     if (i == 0 || t < least) least = t, best = i;
   }
   return best;
