@@ -27,7 +27,9 @@ LUT-3), each next to a plain streaming read of the same number of bytes.
 (block7b_u3 at --batch sequences of N cached tokens each): the stacked q/k/v
 product, the write of its keys and values into the 4-bit cache, attention
 over it, the output product added to the residual stream, the gated gate/up
-product and the down product added to the residual stream.
+product and the down product added to the residual stream.  With --mx the
+weights are in MX blocks (4-bit floats, 8-bit activations), and the step has
+its two norms and its rotation by position too.
 
 --copy-mb N also times a plain elementwise copy of N MiB (a kernel of known
 traffic, used to calibrate the HBM byte counters of a profiler run).
@@ -372,7 +374,7 @@ def measure(torch, qgemv, workload, B, steps, warmup, rotate_gib, stream, dev, u
     return per_layer, alg_total, ms_total, cpu_layers
 
 
-HEADS_7B, HEAD_DIM_7B = 32, 128  # 4096 activations
+HEADS_7B, HEAD_DIM_7B, MLP_7B = 32, 128, 11008  # 4096 activations
 
 
 def step_weights(qgemv):
@@ -437,6 +439,69 @@ def measure_step(torch, qgemv, B, ctx, steps, warmup, rotate_gib, stream, dev, u
         assert torch.isfinite(y).all().item(), "non-finite output"
         assert torch.equal(y, out[0]), "copies disagree"
     return ms, step_bytes(weights, B, ctx, group), copies
+
+
+def mx_step_bytes(B: int, ctx: int, group: int) -> int:
+    """As step_bytes, of the MX step: E2M1 weights and E4M3 activations with their exponents."""
+    E, F = HEADS_7B * HEAD_DIM_7B, MLP_7B
+    weights = (4 * E * E + 3 * E * F) * 17 // 32
+    per_token = 2 * HEADS_7B * (HEAD_DIM_7B // 2 + 4 * HEAD_DIM_7B // group)
+    # FP16: the stream read by two norms and a residual and written twice, q/k/v and the turned queries, attention's
+    # output, o's and the gated product's, each written and read, and the norms' vectors
+    half = 2 * B * (5 * E + 2 * 3 * E + 2 * E + 2 * E + 2 * E + 2 * F) + 2 * 2 * E
+    blocks = 2 * 2 * B * E * 33 // 32  # the norms' outputs
+    return weights + B * (ctx + 1) * per_token + half + blocks
+
+
+def measure_mx_step(torch, B, ctx, steps, warmup, rotate_gib, stream, dev, use_graph):
+    """(ms per step, algorithmic bytes, copies) of the 7B decoder block's token step with weights in MX blocks, both norms
+    and the rotation by position."""
+    from dense_sparse_bit_amd import qcache, qmx, qnorm, qrotary
+    H, D, F, page, group = HEADS_7B, HEAD_DIM_7B, MLP_7B, 64, 32
+    E = H * D
+    shapes = {"qkv": (3 * E, E), "o": (E, E), "gate_up": (2 * F, E), "down": (E, F)}
+    n_pages = -(-ctx // page)
+    per_copy = sum(m * k for m, k in shapes.values()) * 17 // 32 + qcache.cache_bytes(B * n_pages, H, D, page, group)
+    copies = max(2, math.ceil(rotate_gib * (1 << 30) / per_copy))
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(0)
+    rand = lambda *s: torch.randn(s, generator=gen, device=dev)  # noqa: E731
+    weights = {n: rand(*s) * s[1] ** -0.5 for n, s in shapes.items()}
+    pre = [(1 + 0.1 * rand(E)).half() for _ in range(2)]
+    rotary = qrotary.Rotary(10000.0 ** (-torch.arange(D // 2, dtype=torch.float64) / (D // 2)), device=dev)
+    lens = torch.full((B,), ctx, dtype=torch.int32, device=dev)
+    pages = torch.arange(B * n_pages, dtype=torch.int32, device=dev).view(B, n_pages)
+    x = rand(B, E).half()
+    k, v = rand(ctx, H, D).half(), rand(ctx, H, D).half()
+    start = torch.tensor([0, ctx], dtype=torch.int32, device=dev)
+    plans, caches = [], []
+    for _ in range(copies):
+        plans.append({n: qmx.QMx(qmx.quantize(w)) for n, w in weights.items()})
+        caches.append(qcache.QCache(B * n_pages, H, D, page_size=page, group=group, device="cuda:0"))
+        for s in range(B):  # every sequence holds the same keys and values
+            caches[-1].write(k, v, lens[:1], pages[s:s + 1], start)
+    out = [torch.empty_like(x) for _ in range(copies)]
+
+    def step(i):
+        i %= copies
+        p, c = plans[i], caches[i]
+        _, x1 = qnorm.norm(None, x, pre=pre[0], out_type="e4m3", keep_h=False)
+        q, kn, vn = (t.unflatten(1, (H, D)) for t in p["qkv"].run(x1).split(E, dim=1))
+        q = rotary.write(c, q, kn, vn, lens, pages)
+        o = p["o"].run(c.attend(q, lens, pages).view(B, E), "e4m3")
+        h, x2 = qnorm.norm(o, x, pre=pre[1], out_type="e4m3")
+        p["down"].run(p["gate_up"].run(x2, act="silu", gated=True), "e4m3", residual=h, out=out[i])
+
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        for i in range(copies):
+            step(i)
+    torch.cuda.synchronize()
+    ms = time_graph(torch, step, steps, warmup, stream, use_graph=use_graph)
+    for y in out:
+        assert torch.isfinite(y).all().item(), "non-finite output"
+        assert torch.equal(y, out[0]), "copies disagree"
+    return ms, mx_step_bytes(B, ctx, group), copies
 
 
 def read_floor(torch, qgemv, nbytes, steps, warmup, stream, dev):
@@ -596,6 +661,9 @@ def main():
                     help="run the layers that share x (q,k,v; gate,up) as one product over their stacked rows")
     ap.add_argument("--step-ctx", type=int, default=0, metavar="N",
                     help="time a token step of the whole 7B decoder block over N cached tokens per sequence")
+    ap.add_argument("--mx", action="store_true",
+                    help="with --step-ctx: weights in MX blocks (E2M1, activations E4M3), both norms and the rotation by "
+                         "position")
     ap.add_argument("--counter-table", default=None, metavar="CSV",
                     help="only print per-kernel median counters of a rocprofv3 counter run (no GPU)")
     ap.add_argument("--counter-summary", nargs=2, default=None, metavar=("FETCH_CSV", "WRITE_CSV"),
@@ -636,8 +704,14 @@ def main():
 
     if a.step_ctx:
         B = a.batch or DEFAULT_BATCH["block7b_u3"]
-        ms, alg, copies = measure_step(torch, qgemv, B, a.step_ctx, a.steps, a.warmup, a.rotate_gib, stream, dev,
-                                       not a.no_graph)
+        if a.mx:
+            ms, alg, copies = measure_mx_step(torch, B, a.step_ctx, a.steps, a.warmup, a.rotate_gib, stream, dev,
+                                              not a.no_graph)
+            note = "E2M1 weights, E4M3 activations, two norms, rotary positions"
+        else:
+            ms, alg, copies = measure_step(torch, qgemv, B, a.step_ctx, a.steps, a.warmup, a.rotate_gib, stream, dev,
+                                           not a.no_graph)
+            note = WORKLOAD_NOTES["block7b_u3"]
         gbs = alg / (ms * 1e-3) / 1e9
         print(json.dumps({
             "metric": "µs per token step of a 7B decoder block and effective GB/s as % of MI355X HBM peak",
@@ -645,7 +719,7 @@ def main():
             "pct_of_hbm_peak": round(100.0 * gbs / HBM_PEAK_GBS, 2), "n_gpus": 1, "steps": a.steps,
             "warmup": a.warmup, "ms_per_step": round(ms, 6), "higher_is_better": True, "scaling": "weak",
             "vs_baseline": None, "dtype": "fp16", "data": "synthetic",
-            "config": {"workload": f"block7b_u3 token step: {WORKLOAD_NOTES['block7b_u3']}; 4-bit cache of {HEADS_7B} "
+            "config": {"workload": f"{'block7b_mx' if a.mx else 'block7b_u3'} token step: {note}; 4-bit cache of {HEADS_7B} "
                                    f"heads x {HEAD_DIM_7B}, groups of 32, {a.step_ctx} tokens per sequence, batch {B}",
                        "batch": B, "context": a.step_ctx, "copies_rotated": copies,
                        "algorithmic_bytes_per_step": alg}}), flush=True)
