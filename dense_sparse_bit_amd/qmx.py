@@ -59,25 +59,27 @@ def _format(fmt):
 
 def _rows(x, what, at=None):
     """(is fp32, row stride) of an FP16 or fp32 [T, K] tensor with contiguous rows; a stride that does not matter is 0."""
-    f32 = x.dtype == torch.float32
-    if (not f32 and x.dtype != torch.float16) or x.dim() != 2 or (at is not None and x.get_device() != at):
+    f32 = x.dtype is torch.float32
+    strides = x.stride()
+    if (not f32 and x.dtype is not torch.float16) or len(strides) != 2 or (at is not None and x.get_device() != at):
         raise ValueError(f"{what} must be an FP16 or fp32 [T, K] tensor" + ("" if at is None else " on the same device"))
-    ld, one = x.stride()
-    if one != 1 and x.shape[1] > 1:
+    if strides[1] != 1:
         raise ValueError(f"{what} must have contiguous rows")
-    return f32, ld if x.shape[0] > 1 else 0
+    return f32, strides[0] if len(x) > 1 else 0
 
 
 class MxRows:
     """Rows [rows, cols] in MX blocks; data is their memory, in the library's own order."""
 
     def __init__(self, rows, cols, fmt="e2m1", device="cuda"):
-        self.rows, self.cols, self.fmt = int(rows), int(cols), fmt
-        if max(self.rows, self.cols) > _MAX:
+        if rows > _MAX or cols > _MAX:
             raise ValueError("counts are 32-bit")
+        self.rows, self.cols, self.fmt = int(rows), int(cols), fmt
         self._shape = Shape(self.rows, self.cols, _format(fmt))
         n = ctypes.c_size_t(0)
-        _check(lib().qmx_bytes(self._shape, n), "qmx_bytes")
+        st = lib().qmx_bytes(self._shape, n)
+        if st != 0:
+            raise QgemvError(st, "qmx_bytes")
         self.data = torch.empty(n.value, dtype=torch.uint8, device=device)
 
     @classmethod
@@ -120,13 +122,17 @@ class MxRows:
             with _launch(at, stream):
                 return self.values(dtype, out)
         if out is None:
-            if dtype != torch.float16 and dtype != torch.float32:
+            f32, ld = dtype is torch.float32, self.cols
+            if not f32 and dtype is not torch.float16:
                 raise ValueError("dtype must be torch.float16 or torch.float32")
-            out = self.data.new_empty(self.rows, self.cols, dtype=dtype)
-        elif out.shape != (self.rows, self.cols):
-            raise ValueError("out must be [rows, cols]")
-        f32, ld = _rows(out, "out", at)
-        _check(lib().qmx_values(self._shape, self.data.data_ptr(), out.data_ptr(), f32, ld, s), "qmx_values")
+            out = self.data.new_empty(self.rows, ld, dtype=dtype)
+        else:
+            if out.shape != (self.rows, self.cols):
+                raise ValueError("out must be [rows, cols]")
+            f32, ld = _rows(out, "out", at)
+        st = lib().qmx_values(self._shape, self.data.data_ptr(), out.data_ptr(), f32, ld, s)
+        if st != 0:
+            raise QgemvError(st, "qmx_values")
         return out
 
 
@@ -142,11 +148,14 @@ def quantize(x, fmt="e2m1", clip=False, out=None, stream=None):
         with _launch(at, stream):
             return quantize(x, fmt, clip, out)
     f32, ld = _rows(x, "x")
+    T, K = x.shape
     if out is None:
-        out = MxRows(x.shape[0], x.shape[1], fmt, x.device)
-    elif (out.rows, out.cols, out.fmt) != (x.shape[0], x.shape[1], fmt) or out.data.get_device() != at:
+        out = MxRows(T, K, fmt, x.device)
+    elif out.rows != T or out.cols != K or out.fmt != fmt or out.data.get_device() != at:
         raise ValueError("out must have x's shape, the format, and be on x's device")
-    _check(lib().qmx_quantize(out._shape, out.data.data_ptr(), x.data_ptr(), f32, ld, bool(clip), s), "qmx_quantize")
+    st = lib().qmx_quantize(out._shape, out.data.data_ptr(), x.data_ptr(), f32, ld, bool(clip), s)
+    if st != 0:
+        raise QgemvError(st, "qmx_quantize")
     return out
 
 

@@ -106,10 +106,13 @@ class Rotary:
             H = q.shape[1]
             qr = cache._rows(q, H, "q", at)
             if out is None:
-                out = q.new_empty(T, H, cache.head_dim, dtype=torch.float16)
-            elif out.shape != q.shape:
-                raise ValueError("out must be in the shape of q")
-            orow = cache._rows(out, H, "out", at, True)
+                D = cache.head_dim
+                out = q.new_empty(T, H, D, dtype=torch.float16)
+                orow = qcache.Rows(out.data_ptr(), 0, H * D, D)
+            else:
+                if out.shape != q.shape:
+                    raise ValueError("out must be in the shape of q")
+                orow = cache._rows(out, H, "out", at, True)
         elif out is not None:
             raise ValueError("out needs q")
         st = lib().qrotary_write(cache._shape, cache.data.data_ptr(), sq, ro, H, qr, orow, kr, vr, s)
