@@ -396,6 +396,9 @@ __device__ __forceinline__ rsrc_t resource(const uint8_t* p, int64_t bytes) {
 __device__ __forceinline__ void to_lds(rsrc_t r, uint8_t* dst, int voff, int soff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, voff, soff, 0, 0);
 }
+__device__ __forceinline__ int load_dword(rsrc_t r, int voff, int soff) {
+  return (int)__builtin_amdgcn_raw_buffer_load_b32(r, voff, soff, 0);
+}
 // s_waitcnt vmcnt(N) alone.
 template <int N>
 __device__ __forceinline__ void wait_vm() {
@@ -563,21 +566,21 @@ k_mx_tile(Side w, Side x, EpiArg<true> ep, int M, int T, int chunks, int quads, 
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
   // Lane 32 g + n of an operand holds row n of two tiles; its blocks are g and 2 + g of a chunk.
   const int tile = (lane >> 4) & 1, place = 16 * (lane & 15) + 256 * (lane >> 5);
-  const int* ea = (const int*)(w.exps + (place >> 2));
-  const int* eb = (const int*)(x.exps + (place >> 2));
+  const rsrc_t xa = resource(w.exps + (int64_t)a0 * quads * 256, (int64_t)(w.tiles - a0) * quads * 256);
+  const rsrc_t xb = resource(x.exps + (int64_t)b0 * quads * 256, (int64_t)(x.tiles - b0) * quads * 256);
   int oa[AT], ob[BT];
 #pragma unroll
-  for (int i = 0; i < AT; ++i) oa[i] = min(a0 + 2 * (wa * AT + i) + tile, w.tiles - 1) * quads * 64;
+  for (int i = 0; i < AT; ++i) oa[i] = min(2 * (wa * AT + i) + tile, w.tiles - 1 - a0) * quads * 256 + (place >> 2);
 #pragma unroll
-  for (int j = 0; j < BT; ++j) ob[j] = min(b0 + 2 * (wb * BT + j) + tile, x.tiles - 1) * quads * 64;
+  for (int j = 0; j < BT; ++j) ob[j] = min(2 * (wb * BT + j) + tile, x.tiles - 1 - b0) * quads * 256 + (place >> 2);
   int sa[2][AT], sb[2][BT], na[2][AT], nb[2][BT];
   auto exponents = [&](int q) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int i = 0; i < AT; ++i) na[h][i] = ea[oa[i] + q * 64 + 32 * h];
+      for (int i = 0; i < AT; ++i) na[h][i] = load_dword(xa, oa[i] + 128 * h, q * 256);
 #pragma unroll
-      for (int j = 0; j < BT; ++j) nb[h][j] = eb[ob[j] + q * 64 + 32 * h];
+      for (int j = 0; j < BT; ++j) nb[h][j] = load_dword(xb, ob[j] + 128 * h, q * 256);
     }
   };
   auto next_exponents = [&] {
