@@ -791,17 +791,23 @@ hipError_t launch_stream(const RunPlan& p, const Side& a, const Side& b, const E
   return hipGetLastError();
 }
 
-// Tiles of features a workgroup takes: as many as leave work for all CUs, since tokens are read once for all of them.
-// 256 | 1376 | 1792 tiles of 4096 | 4096 | 8192 columns, E2M1, 16 rows: 1 tile 5.2 | 14.0 | 31.3 us, 2 tiles
-// 5.7 | 12.1 | 28.1, 4 tiles 6.3 | 13.3 | 26.9.
+// Tiles of features a workgroup takes: as few as let the card hold all workgroups at once (sixteen waves a CU); a second
+// round costs a whole round's time, and many tiles a workgroup little, since tokens are read once for all of them.  us, 16 rows:
+//   256 tiles x 4096 columns (8 waves), E2M1     1 tile  5.5   2 tiles  6.3   3 tiles  7.2
+//   1376 x 4096, E4M3                            2 tiles 15.4  3 tiles 13.8   4 tiles 17.2   7 tiles 14.1
+//   1792 x 8192 (16 waves), E4M3                 2 tiles 36.6  3 tiles 33.7   4 tiles 29.7   7 tiles 28.1
 template <int FMT, int NB, int ROWS>
 hipError_t stream_by_tiles(const RunPlan& p, const Side& a, const Side& b, const EpiArg<true>& ep, const qmx_input* x,
                            hipStream_t st) {
+  const int at_once = 256 * (p.gw.quads >= 16 ? 1 : 16 / p.gw.quads), rt = (a.tiles + at_once - 1) / at_once;
+  if (rt <= 1) return launch_stream<FMT, 1, NB, ROWS>(p, a, b, ep, x, st);
+  if (rt <= 2 || NB > 1) return launch_stream<FMT, 2, NB, ROWS>(p, a, b, ep, x, st);
   if constexpr (NB == 1) {
-    if (a.tiles >= 1536) return launch_stream<FMT, 4, NB, ROWS>(p, a, b, ep, x, st);
+    if (rt <= 3) return launch_stream<FMT, 3, NB, ROWS>(p, a, b, ep, x, st);
+    if (rt <= 4) return launch_stream<FMT, 4, NB, ROWS>(p, a, b, ep, x, st);
+    return launch_stream<FMT, 7, NB, ROWS>(p, a, b, ep, x, st);
   }
-  if (a.tiles >= 512) return launch_stream<FMT, 2, NB, ROWS>(p, a, b, ep, x, st);
-  return launch_stream<FMT, 1, NB, ROWS>(p, a, b, ep, x, st);
+  return hipErrorInvalidValue;
 }
 
 // Whether the tile kernel's copies through LDS are the faster way for up to 64 rows: it takes about the same time for any
