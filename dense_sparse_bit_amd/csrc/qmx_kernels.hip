@@ -292,15 +292,8 @@ k_mx_stream(Side w, Side x, const void* rows, int64_t ldx, EpiArg<true> ep, int 
 #pragma unroll
     for (int j = 0; j < NB; ++j) acc[i][j] = (floatx4_t){0, 0, 0, 0};
   for (int q = wave; q < quads; q += waves) {
-    u32x4_t A[RT][4];
-    int sa[RT], sb[NB];
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        A[i][c] = __builtin_nontemporal_load((const u32x4_t*)(pa[i] + (int64_t)min(4 * q + c, chunks - 1) * 1024));
-      sa[i] = __builtin_nontemporal_load(ea[i] + q * 64);
-    }
+    // tokens first, which the L2 has sooner than memory the weights (22016 x 4096, 16 rows in E4M3: 13.0 us, last 13.4)
+    int sb[NB];
     u32x4_t B[NB][4][P];
     if constexpr (ROWS == 0) {
 #pragma unroll
@@ -312,7 +305,17 @@ k_mx_stream(Side w, Side x, const void* rows, int64_t ldx, EpiArg<true> ep, int 
             B[j][c][e] = *(const u32x4_t*)(pb[j] + (int64_t)min(4 * q + c, chunks - 1) * (1024 * P) + 1024 * e);
         sb[j] = eb[j][q * 64];
       }
-    } else {
+    }
+    u32x4_t A[RT][4];
+    int sa[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        A[i][c] = __builtin_nontemporal_load((const u32x4_t*)(pa[i] + (int64_t)min(4 * q + c, chunks - 1) * 1024));
+      sa[i] = __builtin_nontemporal_load(ea[i] + q * 64);
+    }
+    if constexpr (ROWS != 0) {
       uint8_t* mine = lds + wave * QuadTokens<FMT>::bytes;
       const int col = 512 * q + 8 * lane;
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -728,9 +731,10 @@ hipError_t launch_quantize(const Geo& g, void* blocks, const void* x, int type, 
   return hipGetLastError();
 }
 
-// Rows that the stream kernel quantises on the way: every workgroup does so for itself.  4096 x 4096 with E2M1, E4M3, us:
-// 1 row 4.3, 4.9 (a launch in front: 6.5, 7.1), 4 rows 5.4, 6.1 (6.5, 7.2), 8 rows 6.7, 7.6 (6.7, 7.4); 28672 x 8192: 1 row
-// 24.6, 24.8 (27.4, 27.6), 4 rows 28.0, 31.4 (27.5, 27.6).
+// Rows that the stream kernel quantises on the way: every workgroup does so for itself, where a launch in front takes 3 us (and
+// as much of the host's time).  us, weights from memory, E2M1 | E4M3 rows:
+//   4096 x 4096    1 row 5.4 | 6.0    4 rows  6.9 |  7.6    16 rows (two launches)  9.5 | 10.6
+//   28672 x 8192   1 row 23.9 | 25.6  4 rows 25.6 | 27.5    16 rows (two launches) 29.8 | 31.3
 bool fused_rows(int T, int x_type) { return x_type != QMX_IN_BLOCKS && T <= 4; }
 
 struct RunPlan {
@@ -811,16 +815,16 @@ hipError_t stream_by_tiles(const RunPlan& p, const Side& a, const Side& b, const
 }
 
 // Whether the tile kernel's copies through LDS are the faster way for up to 64 rows: it takes about the same time for any
-// number of features that fill the CUs once, the stream kernel time by the weight.  E2M1, us, stream | tile:
-//   1 row     22016 x 4096: 10.4 | 11.8   28672 x 8192: 26.4 | 21.7
-//   32 rows   4096 x 11008:  8.7 | 15.8   22016 x 4096: 14.1 | 12.3   28672 x 8192: 28.5 | 22.2
-//   64 rows   4096 x 11008: 11.2 | 15.8   22016 x 4096: 21.2 | 12.4   28672 x 8192: 34.8 | 22.5
-// E4M3 rows cost the tile kernel two MFMAs of twice the time:
-//   32 rows   22016 x 4096: 19.1 | 19.8   28672 x 8192: 34.1 | 33.2
-//   64 rows   4096 x 11008: 18.6 | 36.8   22016 x 4096: 30.1 | 19.9   28672 x 8192: 61.2 | 33.5
+// number of features that fill the CUs once, the stream kernel time by the weight.  us, weights from memory, stream | tile:
+//   E2M1    1 row   22016 x 4096: 11.8 | 12.7   28672 x 8192: 25.8 | 24.4
+//          32 rows  4096 x 11008:  9.4 | 22.8   22016 x 4096: 15.6 | 13.3   28672 x 8192: 34.5 | 26.6
+//          64 rows  4096 x 11008: 12.1 | 24.4   22016 x 4096: 23.2 | 14.0   28672 x 8192: 54.8 | 27.1
+//   E4M3   16 rows  28672 x 8192: 26.7 | 33
+//          32 rows  4096 x 11008: 12.9 | 39.4   22016 x 4096: 20.4 | 20.0   28672 x 8192: 39.7 | 34.0
+//          64 rows  4096 x 11008: 18.4 | 40.0   22016 x 4096: 43.3 | 20.3   28672 x 8192: 77.7 | 34.7
 template <int FMT>
 bool tiles_for_few(int M, int T) {
-  if (FMT == kE4M3) return T > 32 && M >= 12288;
+  if (FMT == kE4M3) return T > 16 && M >= (T > 32 ? 12288 : 24576);
   return M >= (T > 32 ? 8192 : T > 16 ? 16384 : 24576);
 }
 
