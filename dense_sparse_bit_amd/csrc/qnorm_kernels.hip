@@ -256,6 +256,10 @@ int check_array(const qnorm_rows& r, bool vector) {
   if ((uintptr_t)r.data % 16 || (!vector && r.ld % 8)) return QGEMV_ERR_INVALID_ARG;
   return QGEMV_OK;
 }
+// An output at the place of an input: each thread then has to store where it loaded.
+bool shifted(const qnorm_rows& out, const qnorm_rows& in, int rows) {
+  return out.data && out.data == in.data && (out.type != in.type || (rows > 1 && out.ld != in.ld));
+}
 Arr array(const qnorm_rows& r) { return Arr{(char*)r.data, r.type == QGEMV_F32, r.ld}; }
 
 }  // namespace
@@ -271,6 +275,8 @@ extern "C" int qnorm_run(const qnorm_args* p, void* stream) {
   if ((!has_y && !p->h.data) || (!has_y && (p->gate.data || p->post.data))) return QGEMV_ERR_INVALID_ARG;
   if ((p->post_bias.data && !p->post.data) || (p->pre_bias.data && !has_pre)) return QGEMV_ERR_INVALID_ARG;
   if (has_pre != (p->out.data != nullptr) || (!p->out.data && !p->h_out.data)) return QGEMV_ERR_INVALID_ARG;
+  // by_size has a thread for 8 columns of the next power of two, 512 at least: 2^32 are past a launch
+  if ((int64_t)p->rows << (p->cols <= 512 ? 9 : 32 - __builtin_clz(p->cols - 1)) >= 1ll << 35) return QGEMV_ERR_UNSUPPORTED;
   int st;
   for (const qnorm_rows* r : {&p->y, &p->h, &p->gate, &p->h_out})
     if ((st = check_array(*r, false))) return st;
@@ -290,6 +296,9 @@ extern "C" int qnorm_run(const qnorm_args* p, void* stream) {
     if ((st = check_array(p->out, false))) return st;
     if (p->rows > 1 && p->out.ld < p->cols) return QGEMV_ERR_INVALID_ARG;
   }
+  if (p->out.data && p->out.data == p->h_out.data) return QGEMV_ERR_INVALID_ARG;
+  for (const qnorm_rows* r : {&p->h_out, &p->out})
+    if (shifted(*r, p->y, p->rows) || shifted(*r, p->h, p->rows)) return QGEMV_ERR_INVALID_ARG;
   a.y = array(p->y), a.h = array(p->h), a.gate = array(p->gate), a.h_out = array(p->h_out), a.out = array(p->out);
   a.post = array(p->post), a.post_bias = array(p->post_bias), a.pre = array(p->pre), a.pre_bias = array(p->pre_bias);
   a.rows = p->rows, a.cols = p->cols, a.eps = p->eps, a.scale = p->scale;

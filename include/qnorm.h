@@ -44,7 +44,7 @@ typedef struct {
 } qnorm_rows;
 
 /*
- *   rows       0 .. 2^26 (0: nothing is done).
+ *   rows       0 .. 2^26 (0: nothing is done), and fewer than 2^35 / (cols, or 512, to the next power of two).
  *   cols       a multiple of 8 (out in blocks: of 32), 8 .. 32768.
  *   y, h       at least one of them.  Without y, h' = scale * h, and neither gate nor post is given.
  *   gate       or none: 1.  ld 0: a factor per column.
@@ -64,8 +64,8 @@ typedef struct {
 
 /*
  * Errors: INVALID_ARG (null args, misalignment, a combination excluded above, a
- * negative or not finite eps, scale not finite, no output, outputs of overlapping rows),
- * UNSUPPORTED (rows, cols, kind, types), HIP.
+ * negative or not finite eps, scale not finite, no output, outputs of overlapping rows, both outputs in
+ * one place, an output in y's or h's with another type or ld), UNSUPPORTED (rows, cols, kind, types), HIP.
  */
 int qnorm_run(const qnorm_args* args, void* stream);
 

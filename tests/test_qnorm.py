@@ -60,6 +60,18 @@ def test_refused(want, kw):
     assert qnorm.lib().qnorm_run(ctypes.byref(args(**kw)), None) == want
 
 
+@pytest.mark.parametrize("want,kw", [
+    (-3, dict(rows=1 << 26, cols=512)), (-3, dict(rows=1 << 23, cols=2056)), (-3, dict(rows=1 << 20, cols=32768)),  # past a launch
+    (-1, dict(out=R(4096, 0, 64))), (-1, dict(h_out=R(1 << 20, 1, 64))), (-1, dict(h_out=R(1 << 20, 0, 72))),
+    (-1, dict(out=R(1 << 21, 1, 64))), (-1, dict(out=R(1 << 21, 16, 0))), (-1, dict(y=R(), out=R(4096, 0, 64)))])
+def test_outputs_in_the_wrong_place_and_too_many_rows(want, kw):
+    """y at 1 MiB, h at 2 MiB, h_out at 4096, out at 8192 unless given."""
+    a = args(**{**dict(y=R(1 << 20, 0, 64), h=R(1 << 21, 0, 64), out=R(8192, 0, 64)), **kw})
+    for r in (a.y, a.h, a.h_out, a.out):
+        r.ld = r.ld if a.cols == 64 else a.cols
+    assert qnorm.lib().qnorm_run(ctypes.byref(a), None) == want
+
+
 def test_null():
     assert qnorm.lib().qnorm_run(None, None) == -1
 
