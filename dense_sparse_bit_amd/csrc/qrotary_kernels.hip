@@ -288,6 +288,15 @@ int check_turn(const qcache_shape* sh, const qrotary* r) {
   return QGEMV_OK;
 }
 
+// Whether vectors of D elements, T x H of them, may overlap: those of the shorter stride one behind the other, as wholes those of
+// the longer.
+bool overlap(const Rows& r, int64_t T, int64_t H, int64_t D) {
+  if (T == 1 || H == 1) return T * H > 1 && (T > 1 ? r.ts : r.hs) < D;
+  const bool tokens = r.ts < r.hs;
+  const int64_t in = tokens ? r.ts : r.hs, out = tokens ? r.hs : r.ts, n = tokens ? T : H;
+  return in < D || (out - D) / in < n - 1;
+}
+
 struct Launch {
   uint8_t* cache;
   Seqs sq;
@@ -298,13 +307,16 @@ struct Launch {
 template <int D, int NG>
 hipError_t launch(Dims<D, NG>, const Launch& a, uint32_t grid, hipStream_t st) {
   auto go = [&](auto kernel) {
+    // once per instantiation (thread-safe static initialisation): 66 KiB with head_dim 256
+    static const hipError_t attr = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                                       kTable * (D / 2) * 16 + 4 * kTable * key_stride<D>());
+    if (attr != hipSuccess) return attr;
     const size_t lds = (size_t)kTable * a.tn.pairs * 16 + 4 * kTable * key_stride<D>();
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), lds, st, a.cache, a.sq, a.tn, a.q, a.qo, a.k,
                        a.v, a.heads, a.q_heads, a.split);
+    return hipGetLastError();
   };
-  if (a.q.f32) go(k_qrotary_write<D, NG, true>);
-  else go(k_qrotary_write<D, NG, false>);
-  return hipGetLastError();
+  return a.q.f32 ? go(k_qrotary_write<D, NG, true>) : go(k_qrotary_write<D, NG, false>);
 }
 
 }  // namespace
@@ -325,8 +337,7 @@ int qrotary_write(const qcache_shape* shape, void* cache, const qcache_seqs* seq
     if ((st = check_rows(q)) || (st = check_rows(q_out))) return st;
     qr = device_rows(q);
     qo = device_rows(q_out);
-    if ((seqs->n_tok > 1 && qo.ts < shape->head_dim) || (n_q_heads > 1 && qo.hs < shape->head_dim))
-      return QGEMV_ERR_INVALID_ARG;
+    if (overlap(qo, seqs->n_tok, n_q_heads, shape->head_dim)) return QGEMV_ERR_INVALID_ARG;
   }
   const Seqs sq = device_seqs(shape, seqs);
   const Turn tn = {rotary->freqs, rotary->pair_axis, rotary->positions, rotary->rot_dim / 2,

@@ -59,6 +59,18 @@ def test_calls_refused_on_the_host():
     assert call(sh=qcache.Shape(4, 65535, 128, 64, 32), n_seq=1 << 20, n_tok=1 << 20) == -3  # past a launch
 
 
+def test_overlapping_queries_are_refused():
+    """q_out's vectors may lie token by token or head by head, with gaps, and not in each other."""
+    L, sh, ok = qrotary.lib(), qcache.Shape(4, 2, 128, 64, 32), qcache.Rows(4096, 0, 256, 128)
+    r = qrotary._Rotary(8, 0, 1, 4096, None, None)  # refused for rot_dim once all else is in order: -3 comes before q_out
+    assert L.qrotary_write(sh, 4096, qcache.Seqs(5, 5, 1, None, 4096, 4096), r, 3, ok, ok, ok, ok, None) == -3
+    r.rot_dim = 128
+    for ts, hs in [(128, 128), (256, 128), (128, 512), (376, 128), (128, 632), (-512, 128), (512, -128), (8, 1024), (1024, 8),
+                   (0, 128), (640, 0)]:
+        bad = qcache.Rows(4096, 0, ts, hs)
+        assert L.qrotary_write(sh, 4096, qcache.Seqs(5, 5, 1, None, 4096, 4096), r, 3, ok, bad, ok, ok, None) == -1, (ts, hs)
+
+
 # ---------------------------------------------------------------------------
 # GPU
 # ---------------------------------------------------------------------------
