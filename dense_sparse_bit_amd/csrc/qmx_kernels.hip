@@ -25,6 +25,7 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef float floatx16_t __attribute__((ext_vector_type(16)));
 typedef float floatx1_t __attribute__((ext_vector_type(1)));
+typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 
 // ---------------------------------------------------------------------------
 // Quantising, and the values back.
@@ -98,7 +99,7 @@ __device__ __forceinline__ void decode(uint64_t w, float step, float (&v)[N]) {
 }
 
 // Rows leave 16 bytes a lane, lanes side by side: 8 columns of FP16, 4 of fp32 (8 in fp32, two stores with gaps: 8190 x 11008
-// from E4M3 in 106 us, so 95).
+// from E4M3 in 106 us, so 93).
 template <int FMT, bool F32>
 __global__ void __launch_bounds__(256)
 k_mx_values(const uint8_t* __restrict__ blocks, Geo g, void* __restrict__ x, int64_t ldx, int total) {
@@ -245,7 +246,7 @@ __device__ __forceinline__ void put4(const EpiArg<true>& ep, int M, int T, int r
 // registers, and all of a quad's loads are on their way at once.  Their sums meet
 // in LDS and are added in the waves' order.
 //
-// ROWS 1, 2: x comes as FP16 or fp32 rows, 16 at most, and a wave quantises its own
+// ROWS 1, 2: x comes as FP16 or fp32 rows, kFusedRows at most, and a wave quantises its own
 // quads' columns on the way: 8 columns a lane and token, the operands formed by way
 // of LDS.  That saves the launch in front, and its 16 bits a value come from the L2.
 // ---------------------------------------------------------------------------
@@ -254,10 +255,13 @@ constexpr int max_waves() {  // 16 have 128 registers each, 8 have 256
   return (RT + NB * (FMT ? 2 : 1)) * 16 + RT * NB * 4 > 100 ? 8 : 16;
 }
 
+constexpr int kFusedRows = 4;
+
 template <int FMT>
 struct QuadTokens {  // a wave's quantised quad: tokens' codes, then their exponents
   static constexpr int stride = FMT ? 528 : 272;  // bytes of a token, 16 of them for the banks
-  static constexpr int exps = 16 * stride;        // [block q][token] dwords
+  static constexpr int exps = kFusedRows * stride;  // [block q][token] dwords
+  static_assert(kFusedRows <= 16, "a tile");
   static constexpr int bytes = exps + 256;
 };
 
@@ -427,6 +431,11 @@ __device__ __forceinline__ void activate_all(const EpiArg<true>& ep, float (&v)[
   for (int i = 0; i < N; ++i) v[i] = ep.activate(v[i]);
 }
 
+// Whether a lane's eight outputs (four when gated) can be stored, and their residuals loaded, 16 bytes or the whole at a time.
+struct Whole {
+  bool y, residual;
+};
+
 template <class V>
 __device__ __forceinline__ void put_typed(void* y, int f32, int64_t e, V v) {
   constexpr int n = sizeof(V) / 4;
@@ -442,7 +451,7 @@ __device__ __forceinline__ void put_typed(void* y, int f32, int64_t e, V v) {
 // features of a token, U tokens at a time so that their reads and stores overlap.
 template <int AT, int NT>
 __device__ __forceinline__ void put_tile(const EpiArg<true>& ep, int M, int T, int row0, int t0, const float* s, int lane,
-                                         bool whole) {
+                                         Whole whole) {
   constexpr int LT = 2 * AT, RT = 64 / LT;  // lanes of a token, tokens of a round
   constexpr int U = 4;
   const int f = 8 * (lane % LT), row = row0 + f;
@@ -452,7 +461,7 @@ __device__ __forceinline__ void put_tile(const EpiArg<true>& ep, int M, int T, i
   for (int i = 0; i < 8; ++i) bias[i] = ep.bias ? ep.load(ep.bias, ep.bias32, min(row + i, M - 1)) : 0.f;
   const int mo = ep.gated ? M >> 1 : M, col = ep.gated ? row >> 1 : row;
   const int n = min(ep.gated ? 4 : 8, mo - col);
-  const bool full = whole && n == (ep.gated ? 4 : 8);
+  const bool full = n == (ep.gated ? 4 : 8), full_y = full && whole.y, full_r = full && whole.residual;
 #pragma unroll 1
   for (int i0 = lane / LT; i0 < 16 * NT && t0 + i0 < T; i0 += U * RT) {
     float g[U * 8];  // features, or gates
@@ -480,19 +489,37 @@ __device__ __forceinline__ void put_tile(const EpiArg<true>& ep, int M, int T, i
       const int i = i0 + u * RT, t = t0 + i;
       if (i >= 16 * NT || t >= T) continue;
       const int64_t e = t * ep.ldy + col, er = t * ep.ldr + col;
-      if (ep.residual) {
+      if (ep.residual && full_r) {
+        float r[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (ep.res32) {
+          const floatx4_t* from = (const floatx4_t*)((const float*)ep.residual + er);
+          const floatx4_t x = from[0], z = ep.gated ? x : from[1];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) r[k] = x[k], r[4 + k] = z[k];
+        } else if (ep.gated) {
+          const half4_t x = *(const half4_t*)((const _Float16*)ep.residual + er);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) r[k] = (float)x[k];
+        } else {
+          const half8_t x = *(const half8_t*)((const _Float16*)ep.residual + er);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) r[k] = (float)x[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) g[8 * u + k] += r[k];
+      } else if (ep.residual) {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           if (k < n) g[8 * u + k] += ep.load(ep.residual, ep.res32, er + k);
       }
       const floatx4_t a = {g[8 * u], g[8 * u + 1], g[8 * u + 2], g[8 * u + 3]};
       const floatx4_t b = {g[8 * u + 4], g[8 * u + 5], g[8 * u + 6], g[8 * u + 7]};
-      if (full && ep.gated) {
+      if (full_y && ep.gated) {
         put_typed(ep.y, ep.y32, e, a);
-      } else if (full && ep.y32) {
+      } else if (full_y && ep.y32) {
         put_typed(ep.y, 1, e, a);
         put_typed(ep.y, 1, e + 4, b);
-      } else if (full) {
+      } else if (full_y) {
         *(half8_t*)((_Float16*)ep.y + e) = __builtin_convertvector(__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7), half8_t);
       } else {
 #pragma unroll
@@ -529,7 +556,7 @@ __device__ __forceinline__ void tile_of(int id, int tiles_a, int tiles_b, int& t
 
 template <int FMT, int AT, int BT, int S, int WG>
 __global__ void __launch_bounds__(256, WG)
-k_mx_tile(Side w, Side x, EpiArg<true> ep, int M, int T, int chunks, int quads, int tiles_a, int tiles_b, bool whole) {
+k_mx_tile(Side w, Side x, EpiArg<true> ep, int M, int T, int chunks, int quads, int tiles_a, int tiles_b, Whole whole) {
   constexpr int P = FMT ? 2 : 1;               // KiB of a token chunk
   constexpr int CA = 4 * AT, CB = 4 * BT * P;  // KiB of a stage
   constexpr int NL = (CA + CB) / 4;            // copies of a wave and stage
@@ -735,7 +762,7 @@ hipError_t launch_quantize(const Geo& g, void* blocks, const void* x, int type, 
 // as much of the host's time).  us, weights from memory, E2M1 | E4M3 rows:
 //   4096 x 4096    1 row 5.4 | 6.0    4 rows  6.9 |  7.6    16 rows (two launches)  9.5 | 10.6
 //   28672 x 8192   1 row 23.9 | 25.6  4 rows 25.6 | 27.5    16 rows (two launches) 29.8 | 31.3
-bool fused_rows(int T, int x_type) { return x_type != QMX_IN_BLOCKS && T <= 4; }
+bool fused_rows(int T, int x_type) { return x_type != QMX_IN_BLOCKS && T <= kFusedRows; }
 
 struct RunPlan {
   Geo gw, gx;
@@ -758,10 +785,12 @@ int run_plan(const qmx_shape* w, const qmx_input* x, const qgemv_epilogue* e, Ru
   return QGEMV_OK;
 }
 
-// Whether a lane's eight outputs (four when gated) can be stored together, 16 bytes or the whole at a time.
-bool whole_rows(const EpiArg<true>& ep) {
-  const int n = ep.gated || ep.y32 ? 4 : 8, size = ep.y32 ? 4 : 2;
-  return ep.ldy % n == 0 && (uintptr_t)ep.y % (n * size) == 0;
+Whole whole_rows(const EpiArg<true>& ep) {
+  auto whole = [&](const void* p, int64_t ld, int f32) {
+    const int n = ep.gated || f32 ? 4 : 8, size = f32 ? 4 : 2;
+    return ld % n == 0 && (uintptr_t)p % (n * size) == 0;
+  };
+  return Whole{whole(ep.y, ep.ldy, ep.y32), whole(ep.residual, ep.ldr, ep.res32)};
 }
 
 constexpr int kLdsBytes = 160 * 1024;

@@ -339,6 +339,29 @@ def test_epilogue(torch, T, M, K, gated, act):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("res32", [False, True])
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("T,M,K", [(70, 528, 1024), (261, 536, 640)])
+def test_epilogue_of_aligned_rows(torch, T, M, K, gated, f32, res32):
+    """Residuals and outputs whose rows start on 16 bytes, each with and without: loaded and stored whole, or not."""
+    rng = np.random.default_rng(M + T)
+    plan, x, xv, wv = make(torch, rng, T, M, K, "e2m1", False)
+    mo = M // 2 if gated else M
+    res = rng.standard_normal((T, mo)).astype(np.float32 if res32 else np.float16)
+    want, tol = mx.product(xv, wv, None, "silu", gated, res)
+    for gap, off in ((8, 8), (8, 1), (3, 0)):
+        wide = torch.full((T, mo + gap), float("nan"), dtype=torch.float32 if res32 else torch.float16, device="cuda")
+        r = wide[:, off:mo + off] if off + mo <= mo + gap else wide[:, :mo]
+        r.copy_(torch.from_numpy(res))
+        for ogap in (8, 1):
+            out = torch.full((T + 1, mo + ogap), 7.0, dtype=torch.float32 if f32 else torch.float16, device="cuda")
+            plan.run(x, act="silu", gated=gated, residual=r, out=out[:T, :mo])
+            check(out[:T, :mo], want, tol, f32)
+            assert (out[T] == 7).all() and (out[:, mo:] == 7).all()
+
+
+@pytest.mark.gpu
 def test_nan_and_extreme_blocks(torch):
     """A NaN block reaches its own token's, or its own feature's, outputs only; the smallest exponents do not."""
     rng = np.random.default_rng(3)
