@@ -240,11 +240,13 @@ __device__ __forceinline__ void put4(const EpiArg<true>& ep, int M, int T, int r
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: up to 64 tokens (NB tiles of 16), where the weights' way from memory is
-// the time.  A workgroup takes RT tiles of features over all columns; its waves
-// take the quads (512 columns) in turn, straight from memory into the operands'
-// registers, and all of a quad's loads are on their way at once.  Their sums meet
+// Few outputs: one token by any weights, or a few hundred by few features.  A workgroup takes RT tiles of features x NB
+// tiles of tokens over all columns; its waves take the quads (512 columns) in turn, straight from
+// memory into the operands' registers, and all of a quad's loads are on their way at once.  Their sums meet
 // in LDS and are added in the waves' order.
+//
+// A CU takes in RT + NB KiB a chunk (E4M3: RT + 2 NB) for RT NB products, which is the time once the weights' way
+// from memory is not: 61 rows by 4096 x 11008 in 1 x 4 tiles 12.1 us, in 2 x 2, the tokens in two parts, 10.7 (E4M3: 18.8, 14.8).
 //
 // ROWS 1, 2: x comes as FP16 or fp32 rows, kFusedRows at most, and a wave quantises its own
 // quads' columns on the way: 8 columns a lane and token, the operands formed by way
@@ -267,12 +269,15 @@ struct QuadTokens {  // a wave's quantised quad: tokens' codes, then their expon
 
 template <int FMT, int RT, int NB, int ROWS>
 __global__ void __launch_bounds__((64 * max_waves<FMT, RT, NB>()))
-k_mx_stream(Side w, Side x, const void* rows, int64_t ldx, EpiArg<true> ep, int M, int T, int cols, int chunks, int quads) {
+k_mx_stream(Side w, Side x, const void* rows, int64_t ldx, EpiArg<true> ep, int M, int T, int cols, int chunks, int quads, int parts) {
   constexpr int P = FMT ? 2 : 1;
   extern __shared__ __align__(16) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6, n = lane & 15, kq = lane >> 4;
-  const int a0 = blockIdx.x * RT;
+  // workgroups go to the eight XCDs in turn: those of the same features to one, whose L2 shares the weights
+  const int seq = blockIdx.x >> 3, grp = seq / parts;
+  const int a0 = (8 * grp + (blockIdx.x & 7)) * RT, b0 = (seq - grp * parts) * NB;
+  if (a0 >= w.tiles) return;
   const uint8_t *pa[RT], *pb[NB];
   const int *ea[RT], *eb[NB];
 #pragma unroll
@@ -285,7 +290,7 @@ k_mx_stream(Side w, Side x, const void* rows, int64_t ldx, EpiArg<true> ep, int 
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       // tokens past the last read the last one's
-      const int t = min(16 * j + n, T - 1);
+      const int t = min(16 * (b0 + j) + n, T - 1);
       pb[j] = x.codes + (int64_t)(t >> 4) * x.tile_bytes + 256 * kq + 16 * (t & 15);
       eb[j] = (const int*)(x.exps + (int64_t)(t >> 4) * quads * 256) + 16 * kq + (t & 15);
     }
@@ -376,7 +381,7 @@ k_mx_stream(Side w, Side x, const void* rows, int64_t ldx, EpiArg<true> ep, int 
   for (int at = wave; at < RT * NB; at += waves) {
     floatx4_t v = sums[at * 64 + lane];
     for (int k = 1; k < waves; ++k) v += sums[(k * RT * NB + at) * 64 + lane];
-    put4(ep, M, T, (a0 + at / NB) * 16 + 4 * kq, at % NB * 16 + n, v);
+    put4(ep, M, T, (a0 + at / NB) * 16 + 4 * kq, (b0 + at % NB) * 16 + n, v);
   }
 }
 
@@ -816,11 +821,12 @@ hipError_t launch_stream(const RunPlan& p, const Side& a, const Side& b, const E
   const int rounds = (p.gw.quads + most - 1) / most, waves = (p.gw.quads + rounds - 1) / rounds;
   const int sums = waves * RT * NB * 1024, tokens = ROWS ? waves * QuadTokens<FMT>::bytes : 0;
   const int lds = sums > tokens ? sums : tokens;
+  const int groups = ((a.tiles + RT - 1) / RT + 7) / 8, parts = ROWS ? 1 : (b.tiles + NB - 1) / NB;
   auto k = k_mx_stream<FMT, RT, NB, ROWS>;
   static const hipError_t attr = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, kLdsBytes);
   if (attr != hipSuccess) return attr;
-  hipLaunchKernelGGL(k, dim3((a.tiles + RT - 1) / RT), dim3(64 * waves), lds, st, a, b, x->data, x->ldx, ep, p.gw.rows,
-                     p.gx.rows, p.gw.cols, p.gw.chunks, p.gw.quads);
+  hipLaunchKernelGGL(k, dim3(8 * groups * parts), dim3(64 * waves), lds, st, a, b, x->data, x->ldx, ep, p.gw.rows,
+                     p.gx.rows, p.gw.cols, p.gw.chunks, p.gw.quads, parts);
   return hipGetLastError();
 }
 
@@ -829,58 +835,66 @@ hipError_t launch_stream(const RunPlan& p, const Side& a, const Side& b, const E
 //   256 tiles x 4096 columns (8 waves), E2M1     1 tile  5.5   2 tiles  6.3   3 tiles  7.2
 //   1376 x 4096, E4M3                            2 tiles 15.4  3 tiles 13.8   4 tiles 17.2   7 tiles 14.1
 //   1792 x 8192 (16 waves), E4M3                 2 tiles 36.6  3 tiles 33.7   4 tiles 29.7   7 tiles 28.1
-template <int FMT, int NB, int ROWS>
+template <int FMT, int ROWS>
 hipError_t stream_by_tiles(const RunPlan& p, const Side& a, const Side& b, const EpiArg<true>& ep, const qmx_input* x,
                            hipStream_t st) {
   const int at_once = 256 * (p.gw.quads >= 16 ? 1 : 16 / p.gw.quads), rt = (a.tiles + at_once - 1) / at_once;
-  if (rt <= 1) return launch_stream<FMT, 1, NB, ROWS>(p, a, b, ep, x, st);
-  if (rt <= 2 || NB > 1) return launch_stream<FMT, 2, NB, ROWS>(p, a, b, ep, x, st);
-  if constexpr (NB == 1) {
-    if (rt <= 3) return launch_stream<FMT, 3, NB, ROWS>(p, a, b, ep, x, st);
-    if (rt <= 4) return launch_stream<FMT, 4, NB, ROWS>(p, a, b, ep, x, st);
-    return launch_stream<FMT, 7, NB, ROWS>(p, a, b, ep, x, st);
-  }
-  return hipErrorInvalidValue;
+  if (rt <= 1) return launch_stream<FMT, 1, 1, ROWS>(p, a, b, ep, x, st);
+  if (rt <= 2) return launch_stream<FMT, 2, 1, ROWS>(p, a, b, ep, x, st);
+  if (rt <= 3) return launch_stream<FMT, 3, 1, ROWS>(p, a, b, ep, x, st);
+  if (rt <= 4) return launch_stream<FMT, 4, 1, ROWS>(p, a, b, ep, x, st);
+  return launch_stream<FMT, 7, 1, ROWS>(p, a, b, ep, x, st);
 }
 
-// Whether the tile kernel's copies through LDS are the faster way for up to 64 rows: it takes about the same time for any
-// number of features that fill the CUs once, the stream kernel time by the weight.  us, weights from memory, stream | tile:
-//   E2M1    1 row   22016 x 4096: 11.8 | 12.7   28672 x 8192: 25.8 | 24.4
-//          32 rows  4096 x 11008:  9.4 | 22.8   22016 x 4096: 15.6 | 13.3   28672 x 8192: 34.5 | 26.6
-//          64 rows  4096 x 11008: 12.1 | 24.4   22016 x 4096: 23.2 | 14.0   28672 x 8192: 54.8 | 27.1
-//   E4M3   16 rows  28672 x 8192: 26.7 | 33
-//          32 rows  4096 x 11008: 12.9 | 39.4   22016 x 4096: 20.4 | 20.0   28672 x 8192: 39.7 | 34.0
-//          64 rows  4096 x 11008: 18.4 | 40.0   22016 x 4096: 43.3 | 20.3   28672 x 8192: 77.7 | 34.7
-template <int FMT>
-bool tiles_for_few(int M, int T) {
-  if (FMT == kE4M3) return T > 16 && M >= (T > 32 ? 12288 : 24576);
-  return M >= (T > 32 ? 8192 : T > 16 ? 16384 : 24576);
-}
-
-// The tile shape of the least time by a model: so much for a call, and for a workgroup `end` and `chunk` a chunk where two
-// share a CU, `alone` a chunk at least where one has it for itself; a quarter of a workgroup's time more for the last ones
-// where there are several to a CU.  In us, fits to products of 4096 x 4096 to 28672 x 8192 with 128 to 2048 rows,
-// which the model meets within 10 %.
+// Kernel and tiles of the least time by a model, in us.
+//
+// The stream kernel: 2.8 for the call, then as many times as workgroups are a CU what their operands take, KiB by KiB, or
+// the weights' way from memory at 4.4 TB/s.  Past 4096 workgroups it is out of the question.
+//
+// The tile kernel: `call`, and as many times as workgroups are a CU `end` and `chunk` a chunk, or `alone` a chunk, which one
+// workgroup takes whose CU waits for its copies.
+//
+// Fits to 17 to 4096 rows by 1024 x 4096 to 28672 x 8192 with weights from memory (202 products in two formats, each by up to ten
+// of these shapes): the choice is 0.5 % slower than the fastest on average, 15 % at most.  us, stream | tile, the best tiles of each:
+//   E2M1   64 rows  4096 x 11008: 10.6 | 19.5    8192 x 8192: 13.0 | 16.2   22016 x 4096: 20.8 | 13.6
+//         256 rows  1024 x  4096:  6.1 |  8.3    4096 x 4096: 13.5 |  8.7
+//   E4M3   64 rows  4096 x 11008: 14.8 | 35.8    8192 x 8192: 17.1 | 28.3   22016 x 4096: 27.7 | 19.5
+//         256 rows  1024 x  4096:  7.5 | 16.2    4096 x 4096: 17.7 | 16.7
 struct TileCost {
   int features, tokens;
   float call, alone, chunk, end;
 };
+struct Choice {
+  int kernel;  // 0: stream, RT = a, NB = b; 1: tile, shape a
+  int a, b;
+};
 template <int FMT>
-int best_tile(int M, int T, int chunks) {
-  static const TileCost e2m1[] = {{64, 64, 4.6f, 0.13f, 0.096f, 1.2f}, {128, 64, 5.2f, 0.185f, 0.169f, 1.4f},
-                                  {128, 128, 6.3f, 0.217f, 0.244f, 2.2f}, {128, 256, 8.7f, 0.37f, 0.443f, 4.2f}};
-  static const TileCost e4m3[] = {{64, 64, 5.3f, 0.37f, 0.243f, 1.2f}, {128, 64, 5.7f, 0.4f, 0.345f, 2.3f},
-                                  {256, 128, 9.3f, 1.1f, 1.07f, 7.6f}};
-  const TileCost* c = FMT ? e4m3 : e2m1;
-  int best = 0;
+Choice best_choice(int M, int T, int chunks) {
+  static const TileCost e2m1[] = {{64, 64, 4.0f, 0.17f, 0.13f, 0.7f}, {128, 64, 4.0f, 0.235f, 0.205f, 0.9f},
+                                  {128, 128, 4.0f, 0.32f, 0.28f, 1.6f}, {128, 256, 3.6f, 0.5f, 0.51f, 2.8f}};
+  static const TileCost e4m3[] = {{64, 64, 4.5f, 0.375f, 0.27f, 0.6f}, {128, 64, 4.6f, 0.43f, 0.41f, 0.2f},
+                                  {256, 128, 5.8f, 1.2f, 1.2f, 1.5f}};
+  auto of_cu = [&](int64_t features, int64_t tokens) {
+    const int64_t n = ((M + features - 1) / features) * ((T + tokens - 1) / tokens);
+    return (float)((n + 255) / 256);
+  };
+  Choice best = {1, 0, 0};
   float least = 0.f;
   for (int i = 0; i < (FMT ? 3 : 4); ++i) {
-    const int64_t n = (int64_t)((M + c[i].features - 1) / c[i].features) * ((T + c[i].tokens - 1) / c[i].tokens);
-    const float of_cu = n <= 256 ? 1.f : (float)n / 256.f + 0.25f;
-    const float share = of_cu * (chunks * c[i].chunk + c[i].end), alone = chunks * c[i].alone;
-    const float t = c[i].call + (share > alone ? share : alone);
-    if (i == 0 || t < least) least = t, best = i;
+    const TileCost& c = (FMT ? e4m3 : e2m1)[i];
+    const float share = of_cu(c.features, c.tokens) * (chunks * c.chunk + c.end), alone = chunks * c.alone;
+    const float t = c.call + (share > alone ? share : alone);
+    if (i == 0 || t < least) least = t, best = {1, i, 0};
   }
+  for (int rt = 1; rt <= 4; ++rt)
+    for (int nb = 1; nb <= 2; ++nb) {
+      const float n = of_cu(16 * rt, 16 * nb);
+      if (n > 16.f) continue;
+      const float operands = n * (rt + (FMT ? 2 : 1) * nb) * (0.2f + 0.0204f * chunks);
+      const float weights = (float)M * chunks * (68.f / 4.4e6f);
+      const float t = 2.8f + (operands > weights ? operands : weights);
+      if (t < least) least = t, best = {0, rt, nb};
+    }
   return best;
 }
 
@@ -889,19 +903,29 @@ hipError_t launch_product(const RunPlan& p, const Side& a, const Side& b, const 
                           hipStream_t st) {
   const int M = p.gw.rows, T = p.gx.rows;
   if (fused_rows(T, x->x_type))
-    return x->x_type == QGEMV_F32 ? stream_by_tiles<FMT, 1, 2>(p, a, b, ep, x, st) : stream_by_tiles<FMT, 1, 1>(p, a, b, ep, x, st);
-  if (T <= 64 && !tiles_for_few<FMT>(M, T)) {
-    if (T <= 16) return stream_by_tiles<FMT, 1, 0>(p, a, b, ep, x, st);
-    if (T <= 32) return stream_by_tiles<FMT, 2, 0>(p, a, b, ep, x, st);
-    return launch_stream<FMT, 1, 4, 0>(p, a, b, ep, x, st);
+    return x->x_type == QGEMV_F32 ? stream_by_tiles<FMT, 2>(p, a, b, ep, x, st) : stream_by_tiles<FMT, 1>(p, a, b, ep, x, st);
+  // 16 rows are the weights' way from memory.  E2M1, 1 row, us, stream | tile: 22016 x 4096 11.8 | 12.7, 28672 x 8192 25.8 | 24.4;
+  // E4M3, 16 rows by the latter 26.7 | 33
+  if (T <= 16 && (FMT == kE4M3 || M < 24576)) return stream_by_tiles<FMT, 0>(p, a, b, ep, x, st);
+  const Choice c = T <= 16 ? Choice{1, 1, 0} : best_choice<FMT>(M, T, p.gw.chunks);
+  if (c.kernel == 0) {
+    switch (2 * c.a + c.b) {
+      case 3: return launch_stream<FMT, 1, 1, 0>(p, a, b, ep, x, st);
+      case 4: return launch_stream<FMT, 1, 2, 0>(p, a, b, ep, x, st);
+      case 5: return launch_stream<FMT, 2, 1, 0>(p, a, b, ep, x, st);
+      case 6: return launch_stream<FMT, 2, 2, 0>(p, a, b, ep, x, st);
+      case 7: return launch_stream<FMT, 3, 1, 0>(p, a, b, ep, x, st);
+      case 8: return launch_stream<FMT, 3, 2, 0>(p, a, b, ep, x, st);
+      case 9: return launch_stream<FMT, 4, 1, 0>(p, a, b, ep, x, st);
+      default: return launch_stream<FMT, 4, 2, 0>(p, a, b, ep, x, st);
+    }
   }
-  const int i = T <= 64 ? 1 : best_tile<FMT>(M, T, p.gw.chunks);
-  if (i == 0) return launch_tile<FMT, 1, 1, FMT ? 5 : 8, 2>(p, a, b, ep, st);
-  if (i == 1) return launch_tile<FMT, 2, 1, FMT ? 4 : 5, 2>(p, a, b, ep, st);
+  if (c.a == 0) return launch_tile<FMT, 1, 1, FMT ? 5 : 8, 2>(p, a, b, ep, st);
+  if (c.a == 1) return launch_tile<FMT, 2, 1, FMT ? 4 : 5, 2>(p, a, b, ep, st);
   if constexpr (FMT == kE4M3) {
     return launch_tile<FMT, 4, 2, 2, 2>(p, a, b, ep, st);
   } else {
-    if (i == 2) return launch_tile<FMT, 2, 2, 4, 2>(p, a, b, ep, st);
+    if (c.a == 2) return launch_tile<FMT, 2, 2, 4, 2>(p, a, b, ep, st);
     return launch_tile<FMT, 2, 4, 3, 2>(p, a, b, ep, st);
   }
 }

@@ -361,6 +361,33 @@ def test_epilogue_of_aligned_rows(torch, T, M, K, gated, f32, res32):
             assert (out[T] == 7).all() and (out[:, mo:] == 7).all()
 
 
+# Counts from which, in one format or both, the library takes each of its kernels' tiles.
+EVERY = [(18, 2054, 416), (33, 2054, 416), (33, 4106, 416), (33, 6002, 160), (50, 1100, 160), (50, 2054, 160), (70, 8202, 160),
+         (100, 5130, 416), (129, 11010, 160), (129, 22018, 160), (193, 1000, 416), (193, 2054, 416), (257, 522, 160),
+         (257, 2054, 416), (500, 28674, 416), (1001, 4106, 160)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("T,M,K", EVERY)
+def test_every_kernel(torch, T, M, K, gated, fmt):
+    rng = np.random.default_rng(M + T)
+    plan, x, xv, wv = make(torch, rng, T, M, K, fmt, False)
+    mo = M // 2 if gated else M
+    bias = rng.standard_normal(M).astype(np.float32)
+    res = rng.standard_normal((T, mo)).astype(np.float16)
+    say(f"[gpu] product T {T} M {M} K {K} {fmt} gated {gated}")
+    out = torch.full((T + 2, mo + 5), 7.0, device="cuda")
+    y = out[1:1 + T, 2:2 + mo]
+    plan.run(x, fmt, torch.from_numpy(bias).cuda(), "silu", gated, torch.from_numpy(res).cuda(), out=y)
+    want, tol = mx.product(xv, wv, bias, "silu", gated, res)
+    check(y, want, tol, True)
+    edge = torch.ones_like(out, dtype=torch.bool)
+    edge[1:1 + T, 2:2 + mo] = False
+    assert (out[edge] == 7).all()
+
+
 @pytest.mark.gpu
 def test_nan_and_extreme_blocks(torch):
     """A NaN block reaches its own token's, or its own feature's, outputs only; the smallest exponents do not."""
