@@ -225,17 +225,72 @@ __device__ __forceinline__ floatx16_t mx_mfma32(i32x8_t a, const Tokens<FMT>& b,
   }
 }
 
+// 2^t (1 + ln 2 lo), the power and its correction of t + lo in two parts.
+__device__ __forceinline__ float exp2_parts(float t, float lo) {
+  const float p = __builtin_amdgcn_exp2f(t);  // 1 ulp; results below 2^-126 are 0
+  return p < INFINITY ? __builtin_fmaf(p, 0.6931471806f * lo, p) : p;
+}
+// v / (1 + e^-z); below z = -200 it is v / inf.
+__device__ __forceinline__ float times_sigmoid(float v, float z) {
+  constexpr float k1 = 1.442695041f, k2 = 1.925963033e-8f;  // log2 e
+  const float x = -fmaxf(z, -200.f), t = x * k1;
+  return v * __builtin_amdgcn_rcpf(1.f + exp2_parts(t, __builtin_fmaf(x, k2, __builtin_fmaf(x, k1, -t))));
+}
+// v erfc(-v / sqrt 2) / 2.  With x = |v| / sqrt 2, (1 + 2 x) e^(x^2) erfc x is smooth in q = (x - 2) / (x + 2) over all x
+// (Shepherd and Laframboise 1981); the polynomial, a fit of degree 10, is within 6e-8, the result within 4e-7.
+__device__ __forceinline__ float gelu_erf(float v) {
+  constexpr float k1 = 0.7213475108f, k2 = 9.62981517e-9f;  // log2 e / 2
+  constexpr float c[] = {0.000155460424f, -0.000183626486f, -0.00138272671f, 0.00104307686f, 0.00867822673f, -0.00794266723f,
+                         -0.0542082563f, 0.164035827f, -0.166031525f, -0.0927630812f, 1.27697837f};
+  const float a = fminf(__builtin_fabsf(v), 20.f), x = a * 0.7071067812f;
+  const float q = __builtin_fmaf(-4.f, __builtin_amdgcn_rcpf(x + 2.f), 1.f);
+  float r = c[0];
+#pragma unroll
+  for (int i = 1; i < 11; ++i) r = __builtin_fmaf(r, q, c[i]);
+  const float h = a * a, l = __builtin_fmaf(a, a, -h), t = h * -k1;
+  const float e = exp2_parts(t, __builtin_fmaf(l, -k1, __builtin_fmaf(h, -k2, __builtin_fmaf(h, -k1, -t))));
+  const float tail = r * e * (0.5f * __builtin_amdgcn_rcpf(__builtin_fmaf(2.f, x, 1.f)));
+  return v * (v < 0.f ? tail : 1.f - tail);
+}
+
+// N values activated under one look at the kind.  0.5 v (1 + tanh u) = v / (1 + e^-2u).  The forms above are short: the library's
+// division, exp and erfc, 32 times over, are several KiB of instructions that a call fetches from memory (one row by 28672 x 8192
+// with gelu_tanh 31.8 us, so 28.2), and tens of instructions an output (2048 rows by 22016 x 4096, none 122 us: gelu 174, so 152;
+// silu 139, 130).
+template <int N>
+__device__ __forceinline__ void activate_all(int act, float (&v)[N]) {
+  if (act == QGEMV_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = times_sigmoid(v[i], v[i]);
+  } else if (act == QGEMV_ACT_GELU_TANH) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = times_sigmoid(v[i], v[i] * __builtin_fmaf(0.07135481627f, v[i] * v[i], 1.595769122f));
+  } else if (act == QGEMV_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = gelu_erf(v[i]);
+  } else if (act == QGEMV_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];  // a NaN stays one
+  }
+}
+
 // The lane's four features of one token.
 __device__ __forceinline__ void put4(const EpiArg<true>& ep, int M, int T, int row, int t, floatx4_t s) {
   if (t >= T) return;
-  if (ep.gated) {
+  float v[4], g[2];
 #pragma unroll
-    for (int i = 0; i < 4; i += 2)
-      if (row + i < M) ep.put_gated(t, row + i, s[i], s[i + 1]);
+  for (int i = 0; i < 4; ++i) v[i] = ep.biased(s[i], min(row + i, M - 1));
+  if (ep.gated) {
+    g[0] = v[0], g[1] = v[2];
+    activate_all(ep.act, g);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (row + 2 * i < M) ep.store(t, (row >> 1) + i, g[i] * v[2 * i + 1]);
   } else {
+    activate_all(ep.act, v);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (row + i < M) ep.put(t, row + i, s[i]);
+      if (row + i < M) ep.store(t, row + i, v[i]);
   }
 }
 
@@ -423,19 +478,6 @@ __device__ __forceinline__ void wave_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// N values activated under one look at the kind.
-template <int N>
-__device__ __forceinline__ void activate_all(const EpiArg<true>& ep, float (&v)[N]) {
-  if (ep.act == QGEMV_ACT_NONE) return;
-  if (ep.act == QGEMV_ACT_SILU) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = v[i] / (1.f + expf(-v[i]));
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = ep.activate(v[i]);
-}
-
 // Whether a lane's eight outputs (four when gated) can be stored, and their residuals loaded, 16 bytes or the whole at a time.
 struct Whole {
   bool y, residual;
@@ -481,13 +523,13 @@ __device__ __forceinline__ void put_tile(const EpiArg<true>& ep, int M, int T, i
       float h[U * 4];
 #pragma unroll
       for (int i = 0; i < U * 4; ++i) h[i] = g[2 * i];
-      activate_all(ep, h);
+      activate_all(ep.act, h);
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i) g[8 * u + i] = h[4 * u + i] * g[8 * u + 2 * i + 1];
     } else {
-      activate_all(ep, g);
+      activate_all(ep.act, g);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
