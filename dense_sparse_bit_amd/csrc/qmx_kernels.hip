@@ -453,6 +453,11 @@ k_mx_stream(Side w, Side x, const void* rows, int64_t ldx, EpiArg<true> ep, int 
 // without bank conflicts.  Operands are read from LDS half a chunk ahead.  One
 // barrier a chunk: behind it the next chunk has landed for all waves, and the place of the
 // one whose operands all waves hold is free.
+//
+// 8192 rows by 28672 x 8192: E2M1 920 us (4.2 PFLOP/s; MFMAs busy for 61 % of the cycles, at the 1.7 GHz that the card's power leaves
+// of 2.4); 2048 rows 248, in E4M3 583, twice the MFMAs and their operands' split.  Two workgroups a CU hide each other's waits:
+// one of 256 x 256 outputs 959 us where two took 940, one that stays for all its tiles 970 (900); rings of 8 to 10 stages, and each
+// workgroup's columns from another start, are no faster.
 // ---------------------------------------------------------------------------
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
@@ -946,10 +951,11 @@ hipError_t launch_product(const RunPlan& p, const Side& a, const Side& b, const 
   const int M = p.gw.rows, T = p.gx.rows;
   if (fused_rows(T, x->x_type))
     return x->x_type == QGEMV_F32 ? stream_by_tiles<FMT, 2>(p, a, b, ep, x, st) : stream_by_tiles<FMT, 1>(p, a, b, ep, x, st);
-  // 16 rows are the weights' way from memory.  E2M1, 1 row, us, stream | tile: 22016 x 4096 11.8 | 12.7, 28672 x 8192 25.8 | 24.4;
-  // E4M3, 16 rows by the latter 26.7 | 33
-  if (T <= 16 && (FMT == kE4M3 || M < 24576)) return stream_by_tiles<FMT, 0>(p, a, b, ep, x, st);
-  const Choice c = T <= 16 ? Choice{1, 1, 0} : best_choice<FMT>(M, T, p.gw.chunks);
+  // 16 rows are the weights' way from memory, which the stream kernel's loads take past the caches.  28672 x 8192, E2M1, 1 row, us,
+  // stream | tile: 25.9 | 24.6 among such calls, but 26.5 | 47 where the caches hold lines that have to be written back first;
+  // 22016 x 4096 11.8 | 12.7; E4M3, 16 rows 26.7 | 33
+  if (T <= 16) return stream_by_tiles<FMT, 0>(p, a, b, ep, x, st);
+  const Choice c = best_choice<FMT>(M, T, p.gw.chunks);
   if (c.kernel == 0) {
     switch (2 * c.a + c.b) {
       case 3: return launch_stream<FMT, 1, 1, 0>(p, a, b, ep, x, st);
