@@ -32,7 +32,7 @@ struct Arr {
 struct NormArgs {
   Arr y, h, gate, post, post_bias, pre, pre_bias, h_out, out;
   Geo g;  // out in blocks
-  int rows, cols;
+  int rows, cols, by_tile;
   float eps, scale, inv_n;
 };
 
@@ -91,8 +91,8 @@ __device__ __forceinline__ void store8(const Arr& a, int64_t row, int col, const
 // once.  Means and mean squares (of the centred values, so nothing cancels) are sums over the
 // lane, the wave, and the row's waves by way of LDS.
 //
-// 8190 rows of 4096 columns take 53 us in FP16 (268 MB, 5.1 TB/s, a copy's rate), 99 us from FP16 with a gate a
-// row and an fp32 stream into E4M3 blocks (437 MB, 4.4); a row of 8192 with both norms 4.9 us: a launch, the loads, two
+// 8190 rows of 4096 columns take 53 us in FP16 (268 MB, 5.1 TB/s, a copy's rate), 88 us from FP16 with a gate a
+// row and an fp32 stream into E4M3 blocks (437 MB, 5.0); a row of 8192 with both norms 4.9 us: a launch, the loads, two
 // sums' meetings.
 // ---------------------------------------------------------------------------
 template <int W>
@@ -116,7 +116,12 @@ k_qnorm(NormArgs a) {
   __shared__ float s_sum[32];
   int turn = 0;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int row = W == 1 ? blockIdx.x * 4 + wave : blockIdx.x;
+  // Workgroups go to the eight XCDs in turn.  by_tile: the 16 rows of a tile of blocks to one, whose L2 then holds whole lines of it
+  // (8190 x 4096 into E4M3 with a gate and an fp32 stream 88 us, otherwise 99, and 42 MB more are written).
+  constexpr int R = W == 1 ? 4 : 1, B = 16 / R;  // rows of a workgroup, workgroups of a tile
+  const int seq = blockIdx.x >> 3;
+  const int group = OUT != 0 && a.by_tile ? (8 * (seq / B) + (blockIdx.x & 7)) * B + seq % B : blockIdx.x;
+  const int row = R * group + (W == 1 ? wave : 0);
   if (row >= a.rows) return;
   const int first = 8 * (W == 1 ? lane : (int)threadIdx.x);
   constexpr int step = 8 * 64 * W;
@@ -228,7 +233,8 @@ k_qnorm(NormArgs a) {
 // ---- host side ----------------------------------------------------------------
 template <int W, int V, bool LAYER>
 hipError_t launch(const NormArgs& a, int out, hipStream_t st) {
-  const int grid = W == 1 ? (a.rows + 3) / 4 : a.rows, threads = W == 1 ? 256 : 64 * W;
+  const int grid = a.by_tile ? (a.rows + 127) / 128 * (W == 1 ? 32 : 128) : W == 1 ? (a.rows + 3) / 4 : a.rows;
+  const int threads = W == 1 ? 256 : 64 * W;
   auto go = [&](auto k) { hipLaunchKernelGGL(k, dim3(grid), dim3(threads), 0, st, a); };
   if (out == 0) go(k_qnorm<W, V, LAYER, 0>);
   else if (out == 1) go(k_qnorm<W, V, LAYER, 1>);
@@ -275,8 +281,8 @@ extern "C" int qnorm_run(const qnorm_args* p, void* stream) {
   if ((!has_y && !p->h.data) || (!has_y && (p->gate.data || p->post.data))) return QGEMV_ERR_INVALID_ARG;
   if ((p->post_bias.data && !p->post.data) || (p->pre_bias.data && !has_pre)) return QGEMV_ERR_INVALID_ARG;
   if (has_pre != (p->out.data != nullptr) || (!p->out.data && !p->h_out.data)) return QGEMV_ERR_INVALID_ARG;
-  // by_size has a thread for 8 columns of the next power of two, 512 at least: 2^32 are past a launch
-  if ((int64_t)p->rows << (p->cols <= 512 ? 9 : 32 - __builtin_clz(p->cols - 1)) >= 1ll << 35) return QGEMV_ERR_UNSUPPORTED;
+  // by_size has a thread for 8 columns of the next power of two, 512 at least, rows in tiles of 16 on eight XCDs: 2^32 are past a launch
+  if (((int64_t)p->rows + 127 & ~127ll) << (p->cols <= 512 ? 9 : 32 - __builtin_clz(p->cols - 1)) >= 1ll << 35) return QGEMV_ERR_UNSUPPORTED;
   int st;
   for (const qnorm_rows* r : {&p->y, &p->h, &p->gate, &p->h_out})
     if ((st = check_array(*r, false))) return st;
@@ -303,6 +309,7 @@ extern "C" int qnorm_run(const qnorm_args* p, void* stream) {
   a.post = array(p->post), a.post_bias = array(p->post_bias), a.pre = array(p->pre), a.pre_bias = array(p->pre_bias);
   a.rows = p->rows, a.cols = p->cols, a.eps = p->eps, a.scale = p->scale;
   a.inv_n = 1.f / (float)p->cols;
+  a.by_tile = out != 0 && p->rows >= 512;  // fewer would fill the XCDs unevenly
   const hipError_t e = p->kind == QNORM_LAYER ? by_size<true>(a, out, (hipStream_t)stream)
                                               : by_size<false>(a, out, (hipStream_t)stream);
   if (e == hipSuccess) return QGEMV_OK;

@@ -44,7 +44,8 @@ typedef struct {
 } qnorm_rows;
 
 /*
- *   rows       0 .. 2^26 (0: nothing is done), and fewer than 2^35 / (cols, or 512, to the next power of two).
+ *   rows       0 .. 2^26 (0: nothing is done), and, to the next multiple of 128, fewer than 2^35 / (cols, or 512, to the next
+ *              power of two).
  *   cols       a multiple of 8 (out in blocks: of 32), 8 .. 32768.
  *   y, h       at least one of them.  Without y, h' = scale * h, and neither gate nor post is given.
  *   gate       or none: 1.  ld 0: a factor per column.

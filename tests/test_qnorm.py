@@ -154,10 +154,14 @@ def test_parts(torch, T, N, kind, what):
         assert none is None and torch.equal(again, got)
 
 
+# rows enough for the tiles of 16 to be dealt out to the XCDs
+MANY = [(512, 96), (525, 512), (641, 992), (1030, 4096), (700, 8192)]
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
 @pytest.mark.parametrize("kind", ["rms", "layer"])
-@pytest.mark.parametrize("T,N", [(1, 32), (5, 160), (17, 2080), (33, 4096), (3, 8224), (2, 32768)])
+@pytest.mark.parametrize("T,N", [(1, 32), (5, 160), (17, 2080), (33, 4096), (3, 8224), (2, 32768)] + MANY)
 def test_blocks(torch, T, N, kind, fmt):
     """out in MX blocks is what quantising the fp32 out gives, whatever the memory held, and the product takes it."""
     _, g = data(torch, T, N, N)
