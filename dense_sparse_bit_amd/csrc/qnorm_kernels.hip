@@ -5,6 +5,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/qnorm.h"
 #include "qgemv_decode.h"
@@ -33,7 +34,8 @@ struct NormArgs {
   Arr y, h, gate, post, post_bias, pre, pre_bias, h_out, out;
   Geo g;  // out in blocks
   int rows, cols, by_tile;
-  float eps, scale, inv_n;
+  float eps, scale;
+  double inv_n;
 };
 
 __device__ __forceinline__ void load8(const Arr& a, int64_t row, int col, float (&v)[8]) {
@@ -71,63 +73,114 @@ __device__ __forceinline__ void of_raw8(const Arr& a, const Raw8& r, float (&v)[
     for (int i = 0; i < 8; ++i) v[i] = (float)x[i];
   }
 }
-__device__ __forceinline__ void store8(const Arr& a, int64_t row, int col, const float (&v)[8]) {
+template <class F>
+__device__ __forceinline__ void store8(const Arr& a, int64_t row, int col, const F (&x)[8]) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = (float)x[i];
   const int64_t e = row * a.ld + col;
   if (a.f32) {
     floatx4_t* p = (floatx4_t*)((float*)a.data + e);
     p[0] = (floatx4_t){v[0], v[1], v[2], v[3]};
     p[1] = (floatx4_t){v[4], v[5], v[6], v[7]};
   } else {
-    half8_t x;
+    half8_t t;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = (_Float16)v[i];
-    *(half8_t*)((_Float16*)a.data + e) = x;
+    for (int i = 0; i < 8; ++i) t[i] = (_Float16)v[i];
+    *(half8_t*)((_Float16*)a.data + e) = t;
   }
 }
 
 // ---------------------------------------------------------------------------
-// W waves take a row; a lane holds V runs of 8 columns of it in fp32 registers
+// W waves take a row; a lane holds V runs of 8 columns of it in registers
 // from the first load to the last store, so every array is read or written
 // once.  Means and mean squares (of the centred values, so nothing cancels) are sums over the
 // lane, the wave, and the row's waves by way of LDS.
 //
-// 8190 rows of 4096 columns take 53 us in FP16 (268 MB, 5.1 TB/s, a copy's rate), 88 us from FP16 with a gate a
-// row and an fp32 stream into E4M3 blocks (437 MB, 5.0); a row of 8192 with both norms 4.9 us: a launch, the loads, two
+// 8190 rows of 4096 columns take 53 us in FP16 (268 MB, 5.1 TB/s, a copy's rate), 94 us from FP16 with a gate a
+// row and an fp32 stream into E4M3 blocks (437 MB, 4.6); a row of 8192 with both norms 4.9 us: a launch, the loads, two
 // sums' meetings.
 // ---------------------------------------------------------------------------
-template <int W>
-__device__ __forceinline__ float row_sum(float v, float* s, int& turn, int wave) {
+__device__ __forceinline__ float mad(float a, float b, float c) { return __builtin_fmaf(a, b, c); }
+__device__ __forceinline__ double mad(double a, double b, double c) { return __builtin_fma(a, b, c); }
+
+// 64 bits by the steps of wave_sum, in two halves.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ double dpp_mov(double v) {
+  const u32x2_t w = __builtin_bit_cast(u32x2_t, v);
+  return __builtin_bit_cast(double, (u32x2_t){(uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[0], CTRL, ROW_MASK, 0xF, false),
+                                              (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[1], CTRL, ROW_MASK, 0xF, false)});
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  v += dpp_mov<0xB1, 0xF>(v);
+  v += dpp_mov<0x4E, 0xF>(v);
+  v += dpp_mov<0x141, 0xF>(v);
+  v += dpp_mov<0x140, 0xF>(v);
+  v += dpp_mov<0x142, 0xA>(v);
+  v += dpp_mov<0x143, 0xC>(v);
+  const u32x2_t w = __builtin_bit_cast(u32x2_t, v);
+  return __builtin_bit_cast(double, (u32x2_t){(uint32_t)__builtin_amdgcn_readlane((int)w[0], 63),
+                                              (uint32_t)__builtin_amdgcn_readlane((int)w[1], 63)});
+}
+
+template <int W, class F>
+__device__ __forceinline__ F row_sum(F v, F* s, int& turn, int wave) {
   v = wave_sum(v);
   if constexpr (W > 1) {
-    float* at = s + (turn ^= 16);  // the other half: the last sum may still be being read
+    F* at = s + (turn ^= 16);  // the other half: the last sum may still be being read
     if ((threadIdx.x & 63) == 0) at[wave] = v;
     __syncthreads();
-    v = 0.f;
+    v = 0;
 #pragma unroll
     for (int i = 0; i < W; ++i) v += at[i];
   }
   return v;
 }
 
-// OUT: 0 rows, 1 E2M1, 2 E4M3.
+// 1 / sqrt(m).  In fp32 in two parts: what the root and the reciprocal round off is the same for the whole row.
+__device__ __forceinline__ void inverse_root(float m, float& r, float& lo) {
+  const float s = sqrtf(m);
+  r = 1.f / s;
+  const float off = __builtin_fmaf(-r, s, 1.f) - 0.5f * (r * r) * __builtin_fmaf(-s, s, m);
+  lo = s > 0.f && s < INFINITY ? r * off : 0.f;
+}
+__device__ __forceinline__ void inverse_root(double m, double& r, double& lo) {
+  r = __builtin_amdgcn_rsq(m);  // to 2^-26 or better; one Newton step doubles the bits
+  lo = r < INFINITY && r > 0.0 ? 0.5 * r * __builtin_fma(-m * r, r, 1.0) : 0.0;
+}
+
+// A double between two floats as the one of them whose last bit is set: what it is rounded to from there, by fewer bits, is what the
+// double is rounded to.  (To the nearest float, 8 of 2^23 values would come to lie in the middle between two E4M3 elements.)
+__device__ __forceinline__ float to_odd(double x) {
+  u32x2_t w = __builtin_bit_cast(u32x2_t, x);
+  const uint32_t rest = ((w[0] & 0x1FFFFFFFu) + 0x1FFFFFFFu) & 0x20000000u;  // the float's last bit, if any below it is set
+  w[0] = (w[0] & 0xE0000000u) | rest;
+  return (float)__builtin_bit_cast(double, w);
+}
+
+// OUT: 0 FP16 rows or none, 1 E2M1, 2 E4M3, 3 fp32 rows.  From 1 on h' and its norm are formed in 64 bits: in fp32 some of
+// 8190 x 4096 values, next to a border between two elements, fall on its other side, and where one is its block's largest the 31
+// others take another step too.  That is 94 us of them into E4M3 (fp32: 88; everything in 64 bits, the norm of y too: 103).
 template <int W, int V, bool LAYER, int OUT>
 __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W)
 k_qnorm(NormArgs a) {
-  __shared__ float s_sum[32];
+  using F = std::conditional_t<OUT == 0, float, double>;
+  __shared__ F s_sum[32];
   int turn = 0;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // Workgroups go to the eight XCDs in turn.  by_tile: the 16 rows of a tile of blocks to one, whose L2 then holds whole lines of it
-  // (8190 x 4096 into E4M3 with a gate and an fp32 stream 88 us, otherwise 99, and 42 MB more are written).
+  // (8190 x 4096 into E4M3 with a gate and an fp32 stream, in fp32, 88 us, otherwise 99, and 42 MB more are written).
   constexpr int R = W == 1 ? 4 : 1, B = 16 / R;  // rows of a workgroup, workgroups of a tile
   const int seq = blockIdx.x >> 3;
-  const int group = OUT != 0 && a.by_tile ? (8 * (seq / B) + (blockIdx.x & 7)) * B + seq % B : blockIdx.x;
+  const int group = (OUT == 1 || OUT == 2) && a.by_tile ? (8 * (seq / B) + (blockIdx.x & 7)) * B + seq % B : blockIdx.x;
   const int row = R * group + (W == 1 ? wave : 0);
   if (row >= a.rows) return;
   const int first = 8 * (W == 1 ? lane : (int)threadIdx.x);
   constexpr int step = 8 * 64 * W;
-  float x[V][8];
+  float y[V][8];
   Raw8 h8[V], g8[V];
-  auto norm = [&](const Arr& weight, const Arr& bias) {
+  auto norm = [&](auto& x, auto* s_sum, const Arr& weight, const Arr& bias) {
+    using F = std::remove_reference_t<decltype(x[0][0])>;
     constexpr bool ahead = V <= 2;  // weights on their way while the sums are formed, where there are registers for them
     Raw8 w8[V], b8[V];
     auto weights = [&](int j, int col) {
@@ -139,28 +192,27 @@ k_qnorm(NormArgs a) {
       for (int j = 0; j < V; ++j)
         if (first + j * step < a.cols) weights(j, first + j * step);
     }
-    float mean = 0.f;
+    const F inv_n = (F)a.inv_n;
+    F mean = 0;
     if constexpr (LAYER) {
-      float sum = 0.f;
+      F sum = 0;
 #pragma unroll
       for (int j = 0; j < V; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum += x[j][i];
-      mean = row_sum<W>(sum, s_sum, turn, wave) * a.inv_n;
+      mean = row_sum<W>(sum, s_sum, turn, wave) * inv_n;
     }
-    float sq = 0.f;
+    F sq = 0;
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if constexpr (LAYER) x[j][i] = first + j * step < a.cols ? x[j][i] - mean : 0.f;
-        sq = __builtin_fmaf(x[j][i], x[j][i], sq);
+        if constexpr (LAYER) x[j][i] = first + j * step < a.cols ? x[j][i] - mean : 0;
+        sq = mad(x[j][i], x[j][i], sq);
       }
-    // 1 / sqrt(m) in two parts: what the root and the reciprocal round off is the same for the whole row
-    const float m = __builtin_fmaf(row_sum<W>(sq, s_sum, turn, wave), a.inv_n, a.eps);
-    const float s = sqrtf(m), r = 1.f / s;
-    const float off = __builtin_fmaf(-r, s, 1.f) - 0.5f * (r * r) * __builtin_fmaf(-s, s, m);
-    const float lo = s > 0.f && s < INFINITY ? r * off : 0.f;
+    F r, lo;
+    inverse_root(mad(row_sum<W>(sq, s_sum, turn, wave), inv_n, (F)a.eps), r, lo);
+    if constexpr (!std::is_same_v<F, float>) r += lo;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int col = first + j * step;
@@ -171,8 +223,8 @@ k_qnorm(NormArgs a) {
       if (bias.data) of_raw8(bias, b8[j], b);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float t = __builtin_fmaf(x[j][i], lo, x[j][i] * r);
-        x[j][i] = bias.data ? __builtin_fmaf(t, w[i], b[i]) : t * w[i];
+        const F t = std::is_same_v<F, float> ? mad(x[j][i], lo, x[j][i] * r) : x[j][i] * r;
+        x[j][i] = bias.data ? mad(t, (F)w[i], (F)b[i]) : t * (F)w[i];
       }
     }
   };
@@ -180,48 +232,54 @@ k_qnorm(NormArgs a) {
   for (int j = 0; j < V; ++j) {
     const int col = first + j * step;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[j][i] = 0.f;
+    for (int i = 0; i < 8; ++i) y[j][i] = 0.f;
     if (col >= a.cols) continue;
-    if (a.y.data) load8(a.y, row, col, x[j]);
+    if (a.y.data) load8(a.y, row, col, y[j]);
     if (a.h.data) h8[j] = raw8(a.h, row, col);
     if (a.gate.data) g8[j] = raw8(a.gate, row, col);
   }
-  if (a.post.data) norm(a.post, a.post_bias);
+  if (a.post.data) norm(y, (float*)s_sum, a.post, a.post_bias);
+  F x[V][8];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int col = first + j * step;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[j][i] = y[j][i];
     if (col >= a.cols) continue;
     if (a.gate.data) {
       float gt[8];
       of_raw8(a.gate, g8[j], gt);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[j][i] *= gt[i];
+      for (int i = 0; i < 8; ++i) x[j][i] *= (F)gt[i];
     }
     if (a.h.data) {
       float h[8];
       of_raw8(a.h, h8[j], h);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[j][i] = a.y.data ? __builtin_fmaf(a.scale, h[i], x[j][i]) : a.scale * h[i];
+      for (int i = 0; i < 8; ++i) x[j][i] = a.y.data ? mad((F)a.scale, (F)h[i], x[j][i]) : (F)a.scale * (F)h[i];
     }
     if (a.h_out.data) store8(a.h_out, row, col, x[j]);
   }
   if (!a.pre.data) return;
-  norm(a.pre, a.pre_bias);
+  norm(x, s_sum, a.pre, a.pre_bias);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int col = first + j * step;
-    if constexpr (OUT == 0) {
+    if constexpr (OUT == 0 || OUT == 3) {
       if (col < a.cols) store8(a.out, row, col, x[j]);
     } else {
       // the columns up to the chunk's end are zeros
-      constexpr int F = OUT == 1 ? kE2M1 : kE4M3;
+      constexpr int FMT = OUT == 1 ? kE2M1 : kE4M3;
       if (col >= 128 * a.g.chunks) continue;
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = to_odd(x[j][i]);
       uint32_t w[2];
-      const uint32_t byte = mx_quad<F>(x[j], false, w);
+      const uint32_t byte = mx_quad<FMT>(v, false, w);
       const int tile = row >> 4, r = row & 15, chunk = col >> 7, c = (col & 127) >> 3;
-      uint8_t* to = (uint8_t*)a.out.data + tile * a.g.tile_bytes + (int64_t)chunk * (F ? 2048 : 1024);
-      if constexpr (F == kE2M1) *(uint32_t*)(to + lane_bytes<F>(r, c)) = w[0];
-      else *(u32x2_t*)(to + lane_bytes<F>(r, c)) = (u32x2_t){w[0], w[1]};
+      uint8_t* to = (uint8_t*)a.out.data + tile * a.g.tile_bytes + (int64_t)chunk * (FMT ? 2048 : 1024);
+      if constexpr (FMT == kE2M1) *(uint32_t*)(to + lane_bytes<FMT>(r, c)) = w[0];
+      else *(u32x2_t*)(to + lane_bytes<FMT>(r, c)) = (u32x2_t){w[0], w[1]};
       if ((c & 3) == 0) {
         uint8_t* ex = (uint8_t*)a.out.data + a.g.exps + ((int64_t)tile * a.g.quads + (chunk >> 2)) * 256 + (chunk & 3);
         ex[4 * (16 * (c >> 2) + r)] = (uint8_t)byte;
@@ -238,7 +296,8 @@ hipError_t launch(const NormArgs& a, int out, hipStream_t st) {
   auto go = [&](auto k) { hipLaunchKernelGGL(k, dim3(grid), dim3(threads), 0, st, a); };
   if (out == 0) go(k_qnorm<W, V, LAYER, 0>);
   else if (out == 1) go(k_qnorm<W, V, LAYER, 1>);
-  else go(k_qnorm<W, V, LAYER, 2>);
+  else if (out == 2) go(k_qnorm<W, V, LAYER, 2>);
+  else go(k_qnorm<W, V, LAYER, 3>);
   return hipGetLastError();
 }
 // As many waves a row as have 8 columns a lane: the shortest way through for few rows, and the fewest registers for many
@@ -301,6 +360,7 @@ extern "C" int qnorm_run(const qnorm_args* p, void* stream) {
   } else if (has_pre) {
     if ((st = check_array(p->out, false))) return st;
     if (p->rows > 1 && p->out.ld < p->cols) return QGEMV_ERR_INVALID_ARG;
+    if (p->out.type == QGEMV_F32) out = 3;
   }
   if (p->out.data && p->out.data == p->h_out.data) return QGEMV_ERR_INVALID_ARG;
   for (const qnorm_rows* r : {&p->h_out, &p->out})
@@ -308,8 +368,8 @@ extern "C" int qnorm_run(const qnorm_args* p, void* stream) {
   a.y = array(p->y), a.h = array(p->h), a.gate = array(p->gate), a.h_out = array(p->h_out), a.out = array(p->out);
   a.post = array(p->post), a.post_bias = array(p->post_bias), a.pre = array(p->pre), a.pre_bias = array(p->pre_bias);
   a.rows = p->rows, a.cols = p->cols, a.eps = p->eps, a.scale = p->scale;
-  a.inv_n = 1.f / (float)p->cols;
-  a.by_tile = out != 0 && p->rows >= 512;  // fewer would fill the XCDs unevenly
+  a.inv_n = 1.0 / p->cols;
+  a.by_tile = (out == 1 || out == 2) && p->rows >= 512;  // fewer would fill the XCDs unevenly
   const hipError_t e = p->kind == QNORM_LAYER ? by_size<true>(a, out, (hipStream_t)stream)
                                               : by_size<false>(a, out, (hipStream_t)stream);
   if (e == hipSuccess) return QGEMV_OK;

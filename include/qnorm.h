@@ -10,8 +10,9 @@
  *   norm(x) = x / sqrt(mean(x^2) + eps)                              QNORM_RMS
  *   norm(x) = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps)      QNORM_LAYER
  *
- * Everything is fp32 until one rounding of h' and of out to their types; the
- * second norm takes h' before its rounding.  out may be rows in MX blocks
+ * Everything is fp32, and h' and its norm 64 bits where out is fp32 or blocks,
+ * until one rounding of h' and of out to their types; the second norm takes h'
+ * before its rounding.  out may be rows in MX blocks
  * (qmx.h), which the next product takes.
  *
  * Statuses are qgemv_status; the entry point does not abort, throw, print,
