@@ -12,6 +12,7 @@
 #include "qgemv_internal.h"
 #include "qmx_blocks.h"
 #include "qmx_layout.h"
+#include "qnorm_sums.h"
 
 using namespace qgemv_dev;
 using namespace qmx_dev;
@@ -123,11 +124,13 @@ __device__ __forceinline__ double wave_sum(double v) {
                                               (uint32_t)__builtin_amdgcn_readlane((int)w[1], 63)});
 }
 
+// last: where the row's last sum lies (qnorm_sums.h).
 template <int W, class F>
-__device__ __forceinline__ F row_sum(F v, F* s, int& turn, int wave) {
+__device__ __forceinline__ F row_sum(F v, char* s_sum, int& last, int wave) {
+  static_assert(W <= qnorm_sums::kWaves && W * (int)sizeof(F) <= qnorm_sums::kHalf, "a sum's parts lie in one half");
   v = wave_sum(v);
   if constexpr (W > 1) {
-    F* at = s + (turn ^= 16);  // the other half: the last sum may still be being read
+    F* at = (F*)(s_sum + (last = qnorm_sums::next(last)));
     if ((threadIdx.x & 63) == 0) at[wave] = v;
     __syncthreads();
     v = 0;
@@ -165,8 +168,8 @@ template <int W, int V, bool LAYER, int OUT>
 __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W)
 k_qnorm(NormArgs a) {
   using F = std::conditional_t<OUT == 0, float, double>;
-  __shared__ F s_sum[32];
-  int turn = 0;
+  __shared__ __align__(16) char s_sum[qnorm_sums::kBytes];
+  int last = 0;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // Workgroups go to the eight XCDs in turn.  by_tile: the 16 rows of a tile of blocks to one, whose L2 then holds whole lines of it
   // (8190 x 4096 into E4M3 with a gate and an fp32 stream, in fp32, 88 us, otherwise 99, and 42 MB more are written).
@@ -179,7 +182,7 @@ k_qnorm(NormArgs a) {
   constexpr int step = 8 * 64 * W;
   float y[V][8];
   Raw8 h8[V], g8[V];
-  auto norm = [&](auto& x, auto* s_sum, const Arr& weight, const Arr& bias) {
+  auto norm = [&](auto& x, const Arr& weight, const Arr& bias) {
     using F = std::remove_reference_t<decltype(x[0][0])>;
     constexpr bool ahead = V <= 2;  // weights on their way while the sums are formed, where there are registers for them
     Raw8 w8[V], b8[V];
@@ -200,7 +203,7 @@ k_qnorm(NormArgs a) {
       for (int j = 0; j < V; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum += x[j][i];
-      mean = row_sum<W>(sum, s_sum, turn, wave) * inv_n;
+      mean = row_sum<W>(sum, s_sum, last, wave) * inv_n;
     }
     F sq = 0;
 #pragma unroll
@@ -211,7 +214,7 @@ k_qnorm(NormArgs a) {
         sq = mad(x[j][i], x[j][i], sq);
       }
     F r, lo;
-    inverse_root(mad(row_sum<W>(sq, s_sum, turn, wave), inv_n, (F)a.eps), r, lo);
+    inverse_root(mad(row_sum<W>(sq, s_sum, last, wave), inv_n, (F)a.eps), r, lo);
     if constexpr (!std::is_same_v<F, float>) r += lo;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -238,7 +241,7 @@ k_qnorm(NormArgs a) {
     if (a.h.data) h8[j] = raw8(a.h, row, col);
     if (a.gate.data) g8[j] = raw8(a.gate, row, col);
   }
-  if (a.post.data) norm(y, (float*)s_sum, a.post, a.post_bias);
+  if (a.post.data) norm(y, a.post, a.post_bias);
   F x[V][8];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
@@ -261,7 +264,7 @@ k_qnorm(NormArgs a) {
     if (a.h_out.data) store8(a.h_out, row, col, x[j]);
   }
   if (!a.pre.data) return;
-  norm(x, s_sum, a.pre, a.pre_bias);
+  norm(x, a.pre, a.pre_bias);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int col = first + j * step;
