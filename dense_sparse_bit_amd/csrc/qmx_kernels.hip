@@ -230,10 +230,11 @@ __device__ __forceinline__ float exp2_parts(float t, float lo) {
   const float p = __builtin_amdgcn_exp2f(t);  // 1 ulp; results below 2^-126 are 0
   return p < INFINITY ? __builtin_fmaf(p, 0.6931471806f * lo, p) : p;
 }
-// v / (1 + e^-z); below z = -200 it is v / inf.
+// v / (1 + e^-z); below z = -200 it is v / inf, above 200 v / 1.  Held on both sides: t of a z past fp32's largest / log2 e would be
+// infinite, and its correction then NaN.
 __device__ __forceinline__ float times_sigmoid(float v, float z) {
   constexpr float k1 = 1.442695041f, k2 = 1.925963033e-8f;  // log2 e
-  const float x = -fmaxf(z, -200.f), t = x * k1;
+  const float x = -__builtin_amdgcn_fmed3f(z, -200.f, 200.f), t = x * k1;
   return v * __builtin_amdgcn_rcpf(1.f + exp2_parts(t, __builtin_fmaf(x, k2, __builtin_fmaf(x, k1, -t))));
 }
 // v erfc(-v / sqrt 2) / 2.  With x = |v| / sqrt 2, (1 + 2 x) e^(x^2) erfc x is smooth in q = (x - 2) / (x + 2) over all x
