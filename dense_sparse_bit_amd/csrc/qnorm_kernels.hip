@@ -74,20 +74,27 @@ __device__ __forceinline__ void of_raw8(const Arr& a, const Raw8& r, float (&v)[
     for (int i = 0; i < 8; ++i) v[i] = (float)x[i];
   }
 }
+// A double between two floats as the one of them whose last bit is set: what it is rounded to from there, by fewer bits, is what the
+// double is rounded to.  (To the nearest float, 8 of 2^23 values would come to lie in the middle between two E4M3 elements.)
+__device__ __forceinline__ float to_odd(double x) {
+  u32x2_t w = __builtin_bit_cast(u32x2_t, x);
+  const uint32_t rest = ((w[0] & 0x1FFFFFFFu) + 0x1FFFFFFFu) & 0x20000000u;  // the float's last bit, if any below it is set
+  w[0] = (w[0] & 0xE0000000u) | rest;
+  return (float)__builtin_bit_cast(double, w);
+}
+__device__ __forceinline__ float to_odd(float x) { return x; }
+
 template <class F>
 __device__ __forceinline__ void store8(const Arr& a, int64_t row, int col, const F (&x)[8]) {
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = (float)x[i];
   const int64_t e = row * a.ld + col;
   if (a.f32) {
     floatx4_t* p = (floatx4_t*)((float*)a.data + e);
-    p[0] = (floatx4_t){v[0], v[1], v[2], v[3]};
-    p[1] = (floatx4_t){v[4], v[5], v[6], v[7]};
+    p[0] = (floatx4_t){(float)x[0], (float)x[1], (float)x[2], (float)x[3]};
+    p[1] = (floatx4_t){(float)x[4], (float)x[5], (float)x[6], (float)x[7]};
   } else {
     half8_t t;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = (_Float16)v[i];
+    for (int i = 0; i < 8; ++i) t[i] = (_Float16)to_odd(x[i]);
     *(half8_t*)((_Float16*)a.data + e) = t;
   }
 }
@@ -150,15 +157,6 @@ __device__ __forceinline__ void inverse_root(float m, float& r, float& lo) {
 __device__ __forceinline__ void inverse_root(double m, double& r, double& lo) {
   r = __builtin_amdgcn_rsq(m);  // to 2^-26 or better; one Newton step doubles the bits
   lo = r < INFINITY && r > 0.0 ? 0.5 * r * __builtin_fma(-m * r, r, 1.0) : 0.0;
-}
-
-// A double between two floats as the one of them whose last bit is set: what it is rounded to from there, by fewer bits, is what the
-// double is rounded to.  (To the nearest float, 8 of 2^23 values would come to lie in the middle between two E4M3 elements.)
-__device__ __forceinline__ float to_odd(double x) {
-  u32x2_t w = __builtin_bit_cast(u32x2_t, x);
-  const uint32_t rest = ((w[0] & 0x1FFFFFFFu) + 0x1FFFFFFFu) & 0x20000000u;  // the float's last bit, if any below it is set
-  w[0] = (w[0] & 0xE0000000u) | rest;
-  return (float)__builtin_bit_cast(double, w);
 }
 
 // OUT: 0 FP16 rows or none, 1 E2M1, 2 E4M3, 3 fp32 rows.  From 1 on h' and its norm are formed in 64 bits: in fp32 some of
