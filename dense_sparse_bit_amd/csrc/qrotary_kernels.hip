@@ -96,10 +96,15 @@ __device__ __forceinline__ void store_run(const Rows& r, int64_t e, const float 
   }
 }
 
+// In the place of the cosine of a pair without an axis, which is left as it is: cosine 1 and sine 0 would make it NaN where its partner is
+// not finite.
+constexpr double kStays = 2.0;
+
 __device__ __forceinline__ void turn(float& a, float& b, doublex2_t cs) {
   const double x = a, y = b;
-  a = (float)__builtin_fma(x, cs[0], -(y * cs[1]));
-  b = (float)__builtin_fma(y, cs[0], x * cs[1]);
+  const bool stays = cs[0] == kStays;
+  a = stays ? a : (float)__builtin_fma(x, cs[0], -(y * cs[1]));
+  b = stays ? b : (float)__builtin_fma(y, cs[0], x * cs[1]);
 }
 
 // What a lane takes of a head of D dimensions: two runs of 8, the two that turn together or two neighbours.
@@ -263,7 +268,7 @@ k_qrotary_write(uint8_t* __restrict__ cache, Seqs sq, Turn tn, Rows q, Rows qo, 
   if (pair < tn.pairs) {
     const int32_t* pos = tn.positions && turns ? tn.positions + (int64_t)axis * tn.n_tok + row0 : nullptr;
     for (int t = t0 + (threadIdx.x >> tn.log_pairs); t < t1; t += 256 >> tn.log_pairs)
-      s_tab[t * tn.pairs + place(pair, tn.pairs)] = cos_sin(pos ? pos[t] : 16 * x.u + t, f);
+      s_tab[t * tn.pairs + place(pair, tn.pairs)] = turns ? cos_sin(pos ? pos[t] : 16 * x.u + t, f) : (doublex2_t){kStays, 0.0};
   }
   const int h0 = (int)((int64_t)heads * part / split), h1 = (int)((int64_t)heads * (part + 1) / split);
   auto unit = [&](int h) { return cache + unit_at(p, x.u, h, heads, sq.up_shift, L::bytes); };
