@@ -302,6 +302,12 @@ bool overlap(const Rows& r, int64_t T, int64_t H, int64_t D) {
   return in < D || (out - D) / in < n - 1;
 }
 
+// q_out at the place of q: each lane then has to store where it loaded.
+bool shifted(const qcache_rows& out, const qcache_rows& in, int64_t T, int64_t H) {
+  return out.data == in.data && (out.type != in.type || (T > 1 && out.tok_stride != in.tok_stride) ||
+                                 (H > 1 && out.head_stride != in.head_stride));
+}
+
 struct Launch {
   uint8_t* cache;
   Seqs sq;
@@ -343,6 +349,7 @@ int qrotary_write(const qcache_shape* shape, void* cache, const qcache_seqs* seq
     qr = device_rows(q);
     qo = device_rows(q_out);
     if (overlap(qo, seqs->n_tok, n_q_heads, shape->head_dim)) return QGEMV_ERR_INVALID_ARG;
+    if (shifted(*q_out, *q, seqs->n_tok, n_q_heads)) return QGEMV_ERR_INVALID_ARG;
   }
   const Seqs sq = device_seqs(shape, seqs);
   const Turn tn = {rotary->freqs, rotary->pair_axis, rotary->positions, rotary->rot_dim / 2,

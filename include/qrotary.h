@@ -51,7 +51,7 @@ typedef struct {
  * same type and strides, and overlaps nothing else that the call reads or writes.  k, v: as qcache_write, n_heads
  * heads; they are not changed.  A row that is on no page is turned all the same.
  * Errors: as qcache_write, plus INVALID_ARG (null or misaligned arrays, positions NULL with axes above 1, q_out
- * of overlapping vectors), UNSUPPORTED (rot_dim, style, axes, n_q_heads).
+ * of overlapping vectors, or in q's place with another type or stride), UNSUPPORTED (rot_dim, style, axes, n_q_heads).
  */
 int qrotary_write(const qcache_shape* shape, void* cache, const qcache_seqs* seqs, const qrotary* rotary,
                   int32_t n_q_heads, const qcache_rows* q, const qcache_rows* q_out, const qcache_rows* k,
