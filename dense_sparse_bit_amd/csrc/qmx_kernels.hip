@@ -1058,6 +1058,8 @@ int qmx_run(const qmx_shape* w, const void* w_blocks, const qmx_input* x, void* 
   if (bad_blocks(w_blocks) || !y) return QGEMV_ERR_INVALID_ARG;
   EpiArg<true> ep;
   if ((st = fill_epilogue(w->rows, y, e, ep))) return st;
+  // the residual at y: each lane then has to store where it loaded
+  if (ep.residual == y && (ep.res32 != ep.y32 || (x->rows > 1 && ep.ldr != ep.ldy))) return QGEMV_ERR_INVALID_ARG;
   const void* xb = x->data;
   if (x->x_type == QMX_IN_BLOCKS) {
     if (bad_blocks(xb)) return QGEMV_ERR_INVALID_ARG;
