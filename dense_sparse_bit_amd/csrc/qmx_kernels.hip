@@ -12,6 +12,7 @@
 #include "qgemv_internal.h"
 #include "qmx_blocks.h"
 #include "qmx_layout.h"
+#include "qmx_ring.h"
 
 using namespace qmx_layout;
 using namespace qmx_dev;
@@ -711,7 +712,8 @@ k_mx_tile(Side w, Side x, EpiArg<true> ep, int M, int T, int chunks, int quads, 
   typedef std::integral_constant<int, 1> I1;
   typedef std::integral_constant<int, 2> I2;
   typedef std::integral_constant<int, 3> I3;
-  auto step = [&](auto J, int q) {
+  // more: another quad follows, and its exponents are loaded.
+  auto step = [&](auto J, int q, auto more) {
     constexpr int jj = decltype(J)::value;
     const int c = 4 * q + jj;
     __builtin_amdgcn_sched_barrier(0);
@@ -719,13 +721,11 @@ k_mx_tile(Side w, Side x, EpiArg<true> ep, int M, int T, int chunks, int quads, 
     multiply(I0{}, J);
     spread<AT + BT * P, AT * BT * P, 0>();
     __builtin_amdgcn_sched_barrier(0);
-    // The next chunk has landed: of what was issued behind it, S - 2 stages may be on the way, and the next exponents where they
-    // were issued in a later step than it.  (In the same step, jj == S - 1, their order is the compiler's.)
-    wait_vm<(S - 2) * NL + (jj >= 1 && jj < S - 1 ? 2 * (AT + BT) : 0)>();
+    wait_vm<qmx_ring::may_be_on_the_way(S, NL, more ? 2 * (AT + BT) : 0, jj)>();  // the next chunk has landed
     wait_lgkm();  // the chunk's operands are in registers, its place is free for all behind the barrier
     wave_barrier();
     stage(c + S);
-    if constexpr (jj == 0) exponents(min(q + 1, quads - 1));
+    if constexpr (jj == 0 && more) exponents(min(q + 1, quads - 1));
     read(c + 1, I0{});
     multiply(I1{}, J);
     spread<AT + BT * P, AT * BT * P, 1>();
@@ -739,16 +739,16 @@ k_mx_tile(Side w, Side x, EpiArg<true> ep, int M, int T, int chunks, int quads, 
   const int full = chunks >> 2, left = chunks & 3;
   for (int q = 0; q < full; ++q) {
     next_exponents();
-    step(I0{}, q);
-    step(I1{}, q);
-    step(I2{}, q);
-    step(I3{}, q);
+    step(I0{}, q, std::true_type{});
+    step(I1{}, q, std::true_type{});
+    step(I2{}, q, std::true_type{});
+    step(I3{}, q, std::true_type{});
   }
   if (left) {
     next_exponents();
-    step(I0{}, full);
-    if (left > 1) step(I1{}, full);
-    if (left > 2) step(I2{}, full);
+    step(I0{}, full, std::false_type{});
+    if (left > 1) step(I1{}, full, std::false_type{});
+    if (left > 2) step(I2{}, full, std::false_type{});
   }
   wait_vm<0>();  // copies past the end
   wait_lgkm();
