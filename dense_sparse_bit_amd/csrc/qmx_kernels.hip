@@ -258,7 +258,7 @@ __device__ __forceinline__ float gelu_erf(float v) {
 // N values activated under one look at the kind.  0.5 v (1 + tanh u) = v / (1 + e^-2u).  The forms above are short: the library's
 // division, exp and erfc, 32 times over, are several KiB of instructions that a call fetches from memory (one row by 28672 x 8192
 // with gelu_tanh 31.8 us, so 28.2), and tens of instructions an output (2048 rows by 22016 x 4096, none 122 us: gelu 174, so 152;
-// silu 139, 130).
+// silu 139, 130; on another card none 118, gelu 142, silu 122).
 template <int N>
 __device__ __forceinline__ void activate_all(int act, float (&v)[N]) {
   if (act == QGEMV_ACT_SILU) {
@@ -302,8 +302,10 @@ __device__ __forceinline__ void put4(const EpiArg<true>& ep, int M, int T, int r
 // memory into the operands' registers, and all of a quad's loads are on their way at once.  Their sums meet
 // in LDS and are added in the waves' order.
 //
-// A CU takes in RT + NB KiB a chunk (E4M3: RT + 2 NB) for RT NB products, which is the time once the weights' way
-// from memory is not: 61 rows by 4096 x 11008 in 1 x 4 tiles 12.1 us, in 2 x 2, the tokens in two parts, 10.7 (E4M3: 18.8, 14.8).
+// A CU takes in RT + NB KiB a chunk (E4M3: RT + 2 NB) for RT NB products, and the time goes with these once the weights' way
+// from memory is not the longer one: 61 rows by 4096 x 11008 in 1 x 4 tiles 12.1 us, in 2 x 2, the tokens in two parts, 10.7
+// (E4M3: 18.8, 14.8).  At some 50 GB/s a CU, 21 bytes a clock, what bounds it is no path's width but the loads' latency: a wave
+// loads a quad, waits, multiplies, and only then loads its next one.
 //
 // ROWS 1, 2: x comes as FP16 or fp32 rows, kFusedRows at most, and a wave quantises its own
 // quads' columns on the way: 8 columns a lane and token, the operands formed by way
@@ -456,10 +458,11 @@ k_mx_stream(Side w, Side x, const void* rows, int64_t ldx, EpiArg<true> ep, int 
 // barrier a chunk: behind it the next chunk has landed for all waves, and the place of the
 // one whose operands all waves hold is free.
 //
-// 8192 rows by 28672 x 8192: E2M1 920 us (4.2 PFLOP/s; MFMAs busy for 61 % of the cycles, at the 1.7 GHz that the card's power leaves
-// of 2.4); 2048 rows 248, in E4M3 583, twice the MFMAs and their operands' split.  Two workgroups a CU hide each other's waits:
-// one of 256 x 256 outputs 959 us where two took 940, one that stays for all its tiles 970 (900); rings of 8 to 10 stages, and each
-// workgroup's columns from another start, are no faster.
+// 8192 rows by 28672 x 8192 among such calls: E2M1 900 to 920 us (4.2 PFLOP/s; MFMAs busy for 60 % of the cycles, at the 1.7 GHz
+// that the card's power leaves of 2.4); 2048 rows 237 to 248, in E4M3 560 to 583, twice the MFMAs and their operands' split.  Alone,
+// the caches clean, 917, 253 and 590; behind 256 MiB of writes, whose lines have to leave first, 1069, 285 and 698.
+// Two workgroups a CU hide each other's waits: one of 256 x 256 outputs 959 us where two took 940, one that stays for all its
+// tiles 970 (900); rings of 8 to 10 stages, and each workgroup's columns from another start, are no faster.
 // ---------------------------------------------------------------------------
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
@@ -815,6 +818,9 @@ hipError_t launch_quantize(const Geo& g, void* blocks, const void* x, int type, 
 // as much of the host's time).  us, weights from memory, E2M1 | E4M3 rows:
 //   4096 x 4096    1 row 5.4 | 6.0    4 rows  6.9 |  7.6    16 rows (two launches)  9.5 | 10.6
 //   28672 x 8192   1 row 23.9 | 25.6  4 rows 25.6 | 27.5    16 rows (two launches) 29.8 | 31.3
+// From some 8 rows on the launch is the shorter way.  us, E2M1, on the way | two launches:
+//   4096 x 4096    5 rows  6.9 |  7.5   8 rows  9.0 |  8.2   16 rows 12.3 |  9.4
+//   28672 x 8192                        8 rows 29.9 | 29.7   16 rows 40.0 | 31.5
 bool fused_rows(int T, int x_type) { return x_type != QMX_IN_BLOCKS && T <= kFusedRows; }
 
 struct RunPlan {
@@ -878,11 +884,14 @@ hipError_t launch_stream(const RunPlan& p, const Side& a, const Side& b, const E
   return hipGetLastError();
 }
 
-// Tiles of features a workgroup takes: as few as let the card hold all workgroups at once (sixteen waves a CU); a second
+// Tiles of features a workgroup takes: as few as let the card hold all workgroups at once, counted as sixteen waves a CU; a second
 // round costs a whole round's time, and many tiles a workgroup little, since tokens are read once for all of them.  us, 16 rows:
-//   256 tiles x 4096 columns (8 waves), E2M1     1 tile  5.5   2 tiles  6.3   3 tiles  7.2
-//   1376 x 4096, E4M3                            2 tiles 15.4  3 tiles 13.8   4 tiles 17.2   7 tiles 14.1
-//   1792 x 8192 (16 waves), E4M3                 2 tiles 36.6  3 tiles 33.7   4 tiles 29.7   7 tiles 28.1
+//   256 tiles x 4096 columns, E2M1    1 tile  5.5   2 tiles  6.3   3 tiles  7.2
+//   1376 x 4096, E4M3                 2 tiles 15.4  3 tiles 13.8   4 tiles 17.2   7 tiles 14.1
+//   1792 x 8192, E4M3                 2 tiles 36.6  3 tiles 33.7   4 tiles 29.7   7 tiles 28.1
+// The count is not so for kernels of more than 128 registers (max_waves: 7 tiles, and 4 in E4M3), of which a CU holds eight
+// waves, and 5 and 6 tiles, which take 7, are not built.  What that costs: 1792 x 4096 in E4M3 17.6 us by the rule's 4 tiles, 16.1
+// by 7; 1280 x 8192 by the rule's 7 for 5 tiles 23.4 us in E2M1 and 21.8 in E4M3, by 5 19.8 and 20.5.
 template <int FMT, int ROWS>
 hipError_t stream_by_tiles(const RunPlan& p, const Side& a, const Side& b, const EpiArg<true>& ep, const qmx_input* x,
                            hipStream_t st) {

@@ -111,9 +111,10 @@ __device__ __forceinline__ void store8(const Arr& a, int64_t row, int col, const
 // once.  Means and mean squares (of the centred values, so nothing cancels) are sums over the
 // lane, the wave, and the row's waves by way of LDS.
 //
-// 8190 rows of 4096 columns take 53 us in FP16 (268 MB, 5.1 TB/s, a copy's rate), 94 us from FP16 with a gate a
-// row and an fp32 stream into E4M3 blocks (437 MB, 4.6); a row of 8192 with both norms 4.9 us: a launch, the loads, two
-// sums' meetings.
+// Among such calls in a graph, 8190 rows of 4096 columns take 53 us in FP16 (268 MB, 5.0 TB/s, a copy's rate), 93 us from FP16
+// with a gate a row and an fp32 stream into E4M3 blocks (437 MB, 4.7); a row of 8192 with both norms 4.6 us: a launch, the
+// loads, two sums' meetings.  Alone, the caches clean, 49 and 87 us; behind 256 MiB of writes, whose lines have to leave first,
+// 65 and 105.  With an FP16 stream into E4M3 blocks 60 us (236 MB, 3.9): the 64 bits show there.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float mad(float a, float b, float c) { return __builtin_fmaf(a, b, c); }
 __device__ __forceinline__ double mad(double a, double b, double c) { return __builtin_fma(a, b, c); }
@@ -161,13 +162,13 @@ __device__ __forceinline__ void inverse_root(float m, float& r, float& lo) {
   lo = s > 0.f && s < INFINITY ? r * off : 0.f;
 }
 __device__ __forceinline__ void inverse_root(double m, double& r, double& lo) {
-  r = __builtin_amdgcn_rsq(m);  // to 2^-26 or better; one Newton step doubles the bits
+  r = __builtin_amdgcn_rsq(m);  // specified to 2^29 ulp, 2^-23; one Newton step leaves 1.5 times its square, 2^-45
   lo = r < INFINITY && r > 0.0 ? 0.5 * r * __builtin_fma(-m * r, r, 1.0) : 0.0;
 }
 
 // OUT: 0 FP16 rows or none, 1 E2M1, 2 E4M3, 3 fp32 rows.  From 1 on h' and its norm are formed in 64 bits: in fp32 some of
 // 8190 x 4096 values, next to a border between two elements, fall on its other side, and where one is its block's largest the 31
-// others take another step too.  That is 94 us of them into E4M3 (fp32: 88; everything in 64 bits, the norm of y too: 103).
+// others take another step too.  That is 93 us of them into E4M3 (fp32: 88; everything in 64 bits, the norm of y too: 103).
 template <int W, int V, bool LAYER, int OUT>
 __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W)
 k_qnorm(NormArgs a) {

@@ -31,10 +31,10 @@ struct Turn {
 // other side of a rounding border, and with it, where it is a group's end, the
 // group's step.
 //
-// 30021 tokens of 64 query and 8 key/value heads x 128 (1.14 GB): 229 us, 5.0 TB/s, a
-// copy's rate; their writing alone takes 36.  Steps there: 390 with a load, its turn and its store at a time; 270
+// 30021 tokens of 64 query and 8 key/value heads x 128 (1.14 GB): 229 to 234 us among such calls (three axes 240), 4.9 TB/s, a
+// copy's rate; alone, the caches clean, 217, and behind 256 MiB of writes 255.  Their writing alone takes 36.  Steps there: 390 with a load, its turn and its store at a time; 270
 // with four heads' loads at once; 229 with the next heads' loads ahead of the turn, and the keys turned like queries and passed
-// to the lanes that quantise them by way of LDS (155 to 256 registers before, 102 to 146 after).
+// to the lanes that quantise them by way of LDS (155 to 256 registers before, 98 to 147 after).
 // ---------------------------------------------------------------------------
 constexpr int kTable = 16;  // tokens of a unit
 
@@ -360,7 +360,8 @@ int qrotary_write(const qcache_shape* shape, void* cache, const qcache_seqs* seq
   // tokens keeps four heads together.  As many as the CUs hold (head_dim 256: two of them fill a CU's LDS; a step's single
   // tokens gain nothing from more than 512).  4 x 2043 tokens of 32 + 32 heads: 519 workgroups 99 us, 1038 71, 2076 81;
   // 300 tokens of 32 + 8 heads: 21 x 8 workgroups 12.9 us, 21 x 32 15.4; 8 x 512 tokens of 16 + 4 heads x 256: 272
-  // workgroups 32 us, 816 41.
+  // workgroups 33 us, 816 41, where the bytes take 18: two workgroups, eight waves, a CU hide little of their loads' latency (32000
+  // tokens 162, the bytes 139).
   int64_t most = shape->n_heads > n_q_heads ? shape->n_heads : n_q_heads;
   if (seqs->q_start) most = (most + 3) / 4;
   const int64_t want = shape->head_dim == 256 ? 256 : seqs->q_start ? 768 : 512;

@@ -92,8 +92,9 @@ int qmx_run_ws(const qmx_shape* w, const qmx_input* x, const qgemv_epilogue* e, 
  * each.  y overlaps nothing that the call reads, except that it may be the residual
  * itself, with the same type and row stride.
  * Errors: INVALID_ARG (null pointer, misalignment, counts below 1, ldy or ldr
- * shorter than a row, the residual in y's place with another type or row stride), UNSUPPORTED (shape, type, format, activation, gated with
- * an odd M, 2^24 tiles of 64 x 64 outputs or more), SIZE (ws_bytes too small), HIP.
+ * shorter than a row, the residual in y's place with another type or row stride),
+ * UNSUPPORTED (shape, type, format, activation, gated with an odd M, 2^24 tiles
+ * of 64 x 64 outputs or more), SIZE (ws_bytes too small), HIP.
  */
 int qmx_run(const qmx_shape* w, const void* w_blocks, const qmx_input* x, void* y, const qgemv_epilogue* e, void* ws,
             size_t ws_bytes, void* stream);
